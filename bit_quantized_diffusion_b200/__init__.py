@@ -385,6 +385,220 @@ def awq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, sz: torch.Tensor,
     return Y
 
 
+ACTIVATIONS = {None: N.ACT_NONE, "none": N.ACT_NONE, "gelu": N.ACT_GELU, "silu": N.ACT_SILU}
+_TYPES = {torch.bfloat16: N.OUT_BF16, torch.float32: N.OUT_F32}
+_E4M3 = torch.float8_e4m3fn
+_INT_MAX = 2 ** 31 - 1
+
+
+def _device() -> int | None:
+    """The current device's index; None where there is none (every tensor is refused then)."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return None
+
+
+def _at(t: torch.Tensor, cur: int | None, name: str) -> int:
+    """A tensor's device address; it lies on the current device (index cur)."""
+    if t.get_device() != cur:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        raise ValueError(f"{name} on {t.device}, but the current device is cuda:{cur}: "
+                         f"call under torch.cuda.device({t.device})")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, rows: int, cols: int, dtype, cur: int, name: str) -> tuple[int, int]:
+    """Address and row stride of a [rows, cols] tensor whose rows are contiguous."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {dtype} [{rows}, {cols}]")
+    ld = t.stride(0) if rows > 1 else cols
+    if t.stride(1) != 1 or not 0 <= ld <= _INT_MAX:
+        raise ValueError(f"{name}: rows must be contiguous, their stride below 2^31")
+    return _at(t, cur, name), ld
+
+
+def _flat(t: torch.Tensor, shape: tuple, dtype, cur: int, name: str) -> int:
+    """Address of a contiguous tensor of one shape and type."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)}")
+    return _at(t, cur, name)
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """Memory for an output, from the pool of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _quantize_args(X, codes, scale, stream):
+    if X.dim() != 2 or X.dtype not in _TYPES:
+        raise ValueError("X must be a 2-D bf16 or float32 tensor")
+    M, K = X.shape
+    if M < 1 or K < 16 or K % 16 or K > 32768:
+        raise ValueError("X must be [M >= 1, K] with K a multiple of 16, at most 32768")
+    cur = _device()
+    x, ldx = _rows(X, M, K, X.dtype, cur, "X")
+    codes = _new((M, K), _E4M3, X, stream) if codes is None else codes
+    scale = _new((M,), torch.float32, X, stream) if scale is None else scale
+    return (M, K, cur, x, ldx, codes, _flat(codes, (M, K), _E4M3, cur, "codes"), scale,
+            _flat(scale, (M,), torch.float32, cur, "scale"))
+
+
+def w8a8_quantize_act(X: torch.Tensor, codes: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                      stream=None):
+    """Rows of X [M, K] (bf16 or float32, row-strided) as E4M3 codes with a float32 scale
+    each: X ~ codes * scale[:, None]. Weights [N, K] go through it too. Returns
+    (codes float8_e4m3fn [M, K], scale float32 [M])."""
+    M, K, cur, x, ldx, codes, pc, scale, ps = _quantize_args(X, codes, scale, stream)
+    N.check(N.load().w8a8_quantize_act(M, K, x, ldx, _TYPES[X.dtype], pc, ps, _stream(stream)),
+            "w8a8_quantize_act")
+    return codes, scale
+
+
+def w8a8_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor | None = None,
+                          residual: torch.Tensor | None = None, eps: float = 1e-6,
+                          codes: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                          residual_out: torch.Tensor | None = None, stream=None):
+    """h = X + residual; y = h / sqrt(mean(h^2) + eps) * weight; rows of y as E4M3 codes with
+    a float32 scale each. X and residual [M, K] bf16 or float32 (row-strided), weight bf16 [K]
+    or None (1). Returns (codes, scale, residual_out): residual_out is h in X's type
+    (residual or X itself may be passed for it: in place), None without a residual."""
+    M, K, cur, x, ldx, codes, pc, scale, ps = _quantize_args(X, codes, scale, stream)
+    pr = po = None
+    ldr = ldo = 0
+    if residual is not None:
+        if residual_out is None:
+            residual_out = _new((M, K), X.dtype, X, stream)
+        pr, ldr = _rows(residual, M, K, X.dtype, cur, "residual")
+        po, ldo = _rows(residual_out, M, K, X.dtype, cur, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    pw = None if weight is None else _flat(weight, (K,), torch.bfloat16, cur, "weight")
+    N.check(N.load().w8a8_rmsnorm_quantize(M, K, x, ldx, pr, ldr, pw, eps, po, ldo, _TYPES[X.dtype], pc, ps,
+                                           _stream(stream)), "w8a8_rmsnorm_quantize")
+    return codes, scale, residual_out
+
+
+def _w8a8_args(a_codes, a_scale, w_codes, w_scale, bias, gated, activation, out_dtype, Y, stream):
+    if a_codes.dim() != 2 or w_codes.dim() != 2:
+        raise ValueError("a_codes and w_codes must be [M, K] and [N, K]")
+    M, K = a_codes.shape
+    rows = w_codes.shape[0]
+    Nc = rows // 2 if gated else rows
+    if M < 1 or K < 16 or K % 16 or Nc < 16 or Nc % 16 or (gated and rows % 32):
+        raise ValueError("M must be at least 1, K and the output's width multiples of 16")
+    if out_dtype not in _TYPES:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}")
+    cur = _device()
+    if Y is None:
+        Y = _new((M, Nc), out_dtype, a_codes, stream)
+    y, ldy = _rows(Y, M, Nc, out_dtype, cur, "Y")
+    return (M, Nc, K, _flat(a_codes, (M, K), _E4M3, cur, "a_codes"), _flat(a_scale, (M,), torch.float32, cur, "a_scale"),
+            _flat(w_codes, (rows, K), _E4M3, cur, "w_codes"),
+            _flat(w_scale, (rows,), torch.float32, cur, "w_scale"),
+            None if bias is None else _flat(bias, (rows,), torch.bfloat16, cur, "bias")), cur, Y, y, ldy
+
+
+def w8a8_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Tensor,
+                bias: torch.Tensor | None = None, residual: torch.Tensor | None = None, activation=None,
+                out_dtype=torch.bfloat16, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [M, N] = act(a_codes w_codes^T * a_scale[:, None] * w_scale + bias) + residual, from
+    the rows of w8a8_quantize_act / w8a8_rmsnorm_quantize: a_codes [M, K], w_codes [N, K]
+    float8_e4m3fn, bias bf16 [N], residual [M, N] of Y's type (Y itself may be passed: in
+    place), activation None, "gelu" (tanh form) or "silu"."""
+    args, cur, Y, y, ldy = _w8a8_args(a_codes, a_scale, w_codes, w_scale, bias, False, activation, out_dtype, Y,
+                                      stream)
+    r, ldr = (None, 0) if residual is None else _rows(residual, args[0], args[1], out_dtype, cur, "residual")
+    N.check(N.load().w8a8_linear(*args, ACTIVATIONS[activation], r, ldr, y, ldy, _TYPES[out_dtype],
+                                 _stream(stream)), "w8a8_linear")
+    return Y
+
+
+def w8a8_gated_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Tensor,
+                      bias: torch.Tensor | None = None, activation="silu", out_dtype=torch.bfloat16,
+                      Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [M, F] = act(gate) * up, where gate | up = a_codes w_codes^T * a_scale[:, None] *
+    w_scale + bias, w_codes [2F, K] holding F gate rows and then F up rows."""
+    args, cur, Y, y, ldy = _w8a8_args(a_codes, a_scale, w_codes, w_scale, bias, True, activation, out_dtype, Y,
+                                      stream)
+    N.check(N.load().w8a8_gated_linear(*args, ACTIVATIONS[activation], y, ldy, _TYPES[out_dtype],
+                                       _stream(stream)), "w8a8_gated_linear")
+    return Y
+
+
+def _rope_args(positions, freq, axis, M, scale, cur):
+    """The arguments svdq_rope and svdq_rope_table share, in their order."""
+    if positions.dtype not in (torch.int32, torch.int64) or positions.dim() not in (1, 2):
+        raise ValueError("positions must be int32 or int64, [M] or [M, axes]")
+    axes = positions.shape[1] if positions.dim() == 2 else 1
+    if positions.shape[0] != M or axes < 1:
+        raise ValueError(f"positions must be [{M}] or [{M}, axes]")
+    if freq.dim() != 1:
+        raise ValueError("freq must be float64 [pairs]")
+    P = freq.shape[0]
+    return (P, axes, _flat(positions, positions.shape, positions.dtype, cur, "positions"),
+            positions.element_size(), _flat(freq, (P,), torch.float64, cur, "freq"),
+            None if axis is None else _flat(axis, (P,), torch.int32, cur, "axis"), float(scale))
+
+
+def _heads(t: torch.Tensor, cur: int, name: str) -> tuple[int, int, int]:
+    """Address, row stride and head stride of a [M, heads, D] tensor with contiguous heads."""
+    M, H, D = t.shape
+    ldh = t.stride(1) if H > 1 else D
+    ld = t.stride(0) if M > 1 else H * ldh
+    if t.stride(2) != 1 or not (0 <= ld <= _INT_MAX and 0 <= ldh <= _INT_MAX):
+        raise ValueError(f"{name}: heads must be contiguous, strides below 2^31")
+    return _at(t, cur, name), ld, ldh
+
+
+def svdq_rope(X: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, axis: torch.Tensor | None = None,
+              scale: float = 1.0, interleaved: bool = False, Y: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """Rotary positions on the heads of X [M, heads, D] (bf16 or float32; row and head strides
+    as they are, e.g. the Q and K heads inside a Q | K | V row): pair i turns by
+    positions[m, axis[i]] * freq[i]. positions int32 or int64 [M] or [M, axes]; freq float64
+    [pairs] (rope_frequencies), 2 pairs <= D, the other columns copied; axis int32 [pairs] or
+    None (0). Pairs are columns (2i, 2i + 1) if interleaved, else (i, i + pairs). ``scale``
+    multiplies cosine and sine. Y may be X (in place)."""
+    if X.dim() != 3 or X.dtype not in _TYPES:
+        raise ValueError("X must be bf16 or float32 [M, heads, D]")
+    M, H, D = X.shape
+    cur = _device()
+    if Y is None:
+        Y = _new((M, H, D), X.dtype, X, stream)
+    if Y.shape != X.shape or Y.dtype != X.dtype:
+        raise ValueError("Y must have X's shape and type")
+    shared = _rope_args(positions, freq, axis, M, scale, cur)
+    if H < 1 or M < 1 or D % 2 or 2 * shared[0] > D:
+        raise ValueError("D must be even and hold 2 * len(freq) columns")
+    N.check(N.load().svdq_rope(M, H, D, *shared, bool(interleaved), _TYPES[X.dtype], *_heads(X, cur, "X"),
+                               *_heads(Y, cur, "Y"), _stream(stream)), "svdq_rope")
+    return Y
+
+
+def svdq_rope_table(positions: torch.Tensor, freq: torch.Tensor, axis: torch.Tensor | None = None,
+                    scale: float = 1.0, angle_major: bool = False, cos: torch.Tensor | None = None,
+                    sin: torch.Tensor | None = None, stream=None):
+    """(cos, sin) float32 [M, pairs] of svdq_rope's angles, or [pairs, M] with angle_major:
+    the layout that svdq_w4a4_linear_qkv_norm_rope takes (64 pairs)."""
+    M = positions.shape[0] if positions.dim() else 0
+    cur = _device()
+    shared = _rope_args(positions, freq, axis, M, scale, cur)
+    shape = (shared[0], M) if angle_major else (M, shared[0])
+    cos = _new(shape, torch.float32, positions, stream) if cos is None else cos
+    sin = _new(shape, torch.float32, positions, stream) if sin is None else sin
+    pc, ps = _flat(cos, shape, torch.float32, cur, "cos"), _flat(sin, shape, torch.float32, cur, "sin")
+    N.check(N.load().svdq_rope_table(M, *shared, bool(angle_major), pc, ps, _stream(stream)), "svdq_rope_table")
+    return cos, sin
+
+
 def svdq_column_absmax(A: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """absmax [K] float32 = max over rows of |A| for a 2-D bf16 tensor A [rows, K]."""
     lib = N.load()

@@ -17,6 +17,7 @@ OK, ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT = ran
 # formats / outputs / pack kinds
 NVFP4_G16, INT4_G64 = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
+ACT_NONE, ACT_GELU, ACT_SILU = 0, 1, 2
 PACK_ACT, PACK_WEIGHT, PACK_AWQ = 0, 1, 2
 
 EXPORTS = (
@@ -28,6 +29,8 @@ EXPORTS = (
     "svdq_w4a4_linear_two_level", "svdq_w4a4_linear_qkv_norm_rope",
     "svdq_column_absmax", "svdq_smoothing", "svdq_lowrank_factors", "svdq_residual",
     "awq_quantize_weight", "svdq_mlp_splits", "svdq_mlp_fc1",
+    "w8a8_quantize_act", "w8a8_rmsnorm_quantize", "w8a8_linear", "w8a8_gated_linear",
+    "svdq_rope", "svdq_rope_table",
 )
 
 _lib = None
@@ -75,6 +78,13 @@ def load() -> ctypes.CDLL:
         "svdq_residual": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P]),
         "awq_quantize_weight": (_I, [_I, _I, _P, _P, _P, _P]),
         "svdq_mlp_splits": (_I, [_I, _I]),
+        "w8a8_quantize_act": (_I, [_I, _I, _P, _I, _I, _P, _P, _P]),
+        "w8a8_rmsnorm_quantize": (_I, [_I, _I, _P, _I, _P, _I, _P, ctypes.c_float, _P, _I, _I, _P, _P, _P]),
+        "w8a8_linear": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _P]),
+        "w8a8_gated_linear": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _P]),
+        "svdq_rope": (_I, [_I, _I, _I, _I, _I, _P, _I, _P, _P, ctypes.c_float, _I, _I, _P, _I, _I, _P, _I, _I,
+                           _P]),
+        "svdq_rope_table": (_I, [_I, _I, _I, _P, _I, _P, _P, ctypes.c_float, _I, _P, _P, _P]),
         "svdq_mlp_fc1": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -19,7 +20,10 @@
 #include "pack.cuh"
 #include "prep.cuh"
 #include "quantize_act.cuh"
+#include "rope.cuh"
 #include "w4a4_gemm.cuh"
+#include "w8a8_gemm.cuh"
+#include "w8a8_quantize.cuh"
 
 namespace {
 
@@ -42,6 +46,7 @@ struct DeviceInfo {
   int gemm_pairs = 0;  // co-resident clusters of the CTA-pair NVFP4 GEMM
   int int4_pairs = 0;  // the same for the INT4 GEMM
   int mlp_pairs = 0;   // the same for the fused MLP's fc1
+  int w8_pairs = 0;    // the same for the 8-bit GEMM
   int gemm_pair_mode = -1;  // -1: by shape; SVDQ_GEMM_PAIR=0/1 forces single-CTA / CTA-pair tiles
   uint32_t* status = nullptr;
   float* xl1_scratch = nullptr;  // device address of g_xl1_scratch
@@ -133,7 +138,11 @@ svdq_status device_setup(DeviceInfo** out) {
     if (cudaFuncSetAttribute(w4a4_int4_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kI4SmemBytes)) != cudaSuccess ||
         cudaFuncSetAttribute(w4a4_mlp_fc1_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kMlSmemBytes)) != cudaSuccess)
+                             static_cast<int>(kMlSmemBytes)) != cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kW8SmemBytes)) != cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kW8SmemBytes)) != cudaSuccess)
       return SVDQ_ERR_CUDA;
     // all of the SM's unified L1/shared storage as shared memory, so that the
     // occupancy the host code plans for (e.g. two quantizer CTAs per SM) is real
@@ -146,6 +155,8 @@ svdq_status device_setup(DeviceInfo** out) {
                           reinterpret_cast<const void*>(w4a4_int4_gemm_kernel<true>),
                           reinterpret_cast<const void*>(awq_gemm_kernel),
                           reinterpret_cast<const void*>(w4a4_mlp_fc1_kernel),
+                          reinterpret_cast<const void*>(w8a8_gemm_kernel<false>),
+                          reinterpret_cast<const void*>(w8a8_gemm_kernel<true>),
                           reinterpret_cast<const void*>(awq_gemv_kernel<1>),
                           reinterpret_cast<const void*>(awq_gemv_kernel<2>)})
       if (cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -183,6 +194,7 @@ svdq_status device_setup(DeviceInfo** out) {
       d.gemm_pairs = pairs(w4a4_nvfp4_gemm_kernel<true>, kGmThreads, GmCfg<true>::kSmemBytes);
       d.int4_pairs = pairs(w4a4_int4_gemm_kernel<true>, kI4Threads, kI4SmemBytes);
       d.mlp_pairs = pairs(w4a4_mlp_fc1_kernel, kMlThreads, kMlSmemBytes);
+      d.w8_pairs = pairs(w8a8_gemm_kernel<false>, kW8Threads, kW8SmemBytes);
       if (std::getenv("SVDQ_DEBUG") != nullptr)
         std::fprintf(stderr, "svdq: %d SMs, %d / %d co-resident NVFP4 / INT4 GEMM CTA pairs\n",
                      d.num_sms, d.gemm_pairs, d.int4_pairs);
@@ -1068,6 +1080,225 @@ svdq_status awq_quantize_weight(int N, int K, const void* W, void* qweight, void
   if (blocks > 0x7FFFFFFFull) return SVDQ_ERR_UNSUPPORTED;
   awq_quantize_kernel<<<static_cast<unsigned>(blocks), 128, 0, static_cast<cudaStream_t>(stream)>>>(
       static_cast<const uint16_t*>(W), N, K, static_cast<uint32_t*>(qweight), static_cast<uint32_t*>(sz));
+  return launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+// the 8-bit linear and its gated form (N: output columns; gated, the weight has 2 N rows)
+svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_codes, const float* a_scale,
+                             const void* w_codes, const float* w_scale, const void* bias, svdq_act act,
+                             const void* residual, int ldr, void* Y, int ldy, svdq_out out,
+                             svdq_stream_t stream) {
+  if (act != SVDQ_ACT_NONE && act != SVDQ_ACT_GELU && act != SVDQ_ACT_SILU) return SVDQ_ERR_INVALID_ARG;
+  if (out != SVDQ_OUT_BF16 && out != SVDQ_OUT_F32) return SVDQ_ERR_INVALID_ARG;
+  if (M < 1 || N < 16 || N % 16 || K < 16 || K % 16 || ldy < N || (gated && N > INT32_MAX / 2))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!a_codes || !a_scale || !w_codes || !w_scale || !Y || (residual && ldr < N)) return SVDQ_ERR_INVALID_ARG;
+  const size_t esz = out == SVDQ_OUT_F32 ? 4 : 2;
+  if (!aligned16(a_codes) || !aligned16(w_codes) || !aligned16(Y) || (ldy * esz) % 16 || !aligned4(a_scale) ||
+      !aligned4(w_scale) || (bias && (reinterpret_cast<uintptr_t>(bias) & 1u)) ||
+      (residual && (!aligned16(residual) || (ldr * esz) % 16)))
+    return SVDQ_ERR_ALIGNMENT;
+  DeviceInfo* d = nullptr;
+  if (svdq_status st = device_setup(&d); st != SVDQ_OK) return st;
+  CUtensorMap tm_a, tm_b, tm_y;
+  const bool f32 = out == SVDQ_OUT_F32;
+  if (!make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, K, M, K, kW8KStage, kW8BM,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, K, gated ? 2ull * N : N, K, kW8KStage,
+                    kW8BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      // output: 32 x 32 boxes, bf16 rows of 64 B (64-byte swizzle) or f32 rows of 128 B
+      !make_tmap_2d(&tm_y, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M,
+                    ldy * esz, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return SVDQ_ERR_CUDA;
+  W8Params p;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  const int tile_n = gated ? kW8BN / 2 : kW8BN;
+  const long long tiles_m = (static_cast<long long>(M) + 2 * kW8BM - 1) / (2 * kW8BM);
+  const long long tiles = tiles_m * ((static_cast<long long>(N) + tile_n - 1) / tile_n);
+  if (tiles > INT32_MAX / 2) return SVDQ_ERR_UNSUPPORTED;
+  p.tiles_m = static_cast<int>(tiles_m);
+  p.tiles = static_cast<int>(tiles);
+  p.act = act == SVDQ_ACT_GELU ? kW8ActGelu : (act == SVDQ_ACT_SILU ? kW8ActSilu : kW8ActNone);
+  p.out_f32 = f32;
+  p.a_scale = a_scale;
+  p.w_scale = w_scale;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.residual = residual;
+  p.ldr = ldr;
+  p.status = d->status;
+  const int units = p.tiles < d->w8_pairs ? p.tiles : d->w8_pairs;
+  auto kern = gated ? w8a8_gemm_kernel<true> : w8a8_gemm_kernel<false>;
+  if (launch_kernel(d, kern, dim3(units * 2), dim3(kW8Threads), kW8SmemBytes, static_cast<cudaStream_t>(stream), 2,
+                    tm_a, tm_b, tm_y, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SVDQ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+svdq_status w8a8_quantize_impl(bool norm, int M, int K, const void* X, int ldx, const void* residual, int ldr,
+                               const void* weight, float eps, void* residual_out, int ldo, svdq_out dtype,
+                               void* codes, float* scale, svdq_stream_t stream) {
+  if (dtype != SVDQ_OUT_BF16 && dtype != SVDQ_OUT_F32) return SVDQ_ERR_INVALID_ARG;
+  if (M < 1 || K < 16 || K % 16 || K > 32768 || ldx < K) return SVDQ_ERR_INVALID_ARG;
+  if (!X || !codes || !scale || (residual != nullptr) != (residual_out != nullptr)) return SVDQ_ERR_INVALID_ARG;
+  if (residual && (ldr < K || ldo < K)) return SVDQ_ERR_INVALID_ARG;
+  if (norm && (!(eps >= 0.0f) || !std::isfinite(eps))) return SVDQ_ERR_INVALID_ARG;
+  const int unit = dtype == SVDQ_OUT_F32 ? 4 : 8;  // elements of 16 bytes
+  if (!aligned16(X) || ldx % unit || !aligned16(codes) || !aligned4(scale) || (weight && !aligned16(weight)) ||
+      (residual && (!aligned16(residual) || !aligned16(residual_out) || ldr % unit || ldo % unit)))
+    return SVDQ_ERR_ALIGNMENT;
+  DeviceInfo* d = nullptr;
+  if (svdq_status st = device_setup(&d); st != SVDQ_OK) return st;
+  W8QuantParams p;
+  p.K = K;
+  p.X = X;
+  p.ldx = ldx;
+  p.residual = residual;
+  p.ldr = ldr;
+  p.residual_out = residual_out;
+  p.ldo = ldo;
+  p.weight = static_cast<const __nv_bfloat16*>(weight);
+  p.eps = eps;
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scale = scale;
+  const bool f32 = dtype == SVDQ_OUT_F32;
+  const int threads = (K / 8 + 127) / 128 * 32;  // four 8-value vectors per thread
+  auto kern = norm ? (f32 ? w8a8_quantize_kernel<true, true, 4> : w8a8_quantize_kernel<true, false, 4>)
+                   : (f32 ? w8a8_quantize_kernel<false, true, 4> : w8a8_quantize_kernel<false, false, 4>);
+  if (launch_kernel(d, kern, dim3(M), dim3(threads), 0, static_cast<cudaStream_t>(stream), 1, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SVDQ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+// the arguments that the rotation and its tables share
+svdq_status rope_params(RopeParams* p, int M, int axes, int pairs, const void* positions, int position_bytes,
+                        const double* freq, const int* axis, float scale) {
+  if (M < 1 || axes < 1 || pairs < 1 || pairs > kRopeMaxPairs || !positions || !freq) return SVDQ_ERR_INVALID_ARG;
+  if ((position_bytes != 4 && position_bytes != 8) || !std::isfinite(scale)) return SVDQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(positions) & (position_bytes - 1)) || (reinterpret_cast<uintptr_t>(freq) & 7u) ||
+      (axis && !aligned4(axis)))
+    return SVDQ_ERR_ALIGNMENT;
+  *p = RopeParams{};
+  p->M = M;
+  p->A = axes;
+  p->P = pairs;
+  p->positions = positions;
+  p->pos64 = position_bytes == 8;
+  p->freq = freq;
+  p->axis = axis;
+  p->scale = scale;
+  return SVDQ_OK;
+}
+
+template <typename T, int V>
+auto rope_kernel_of(bool interleaved) {
+  if constexpr (V > 1) {
+    if (interleaved) return rope_kernel<T, V, true>;
+  }
+  return rope_kernel<T, V, false>;
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status w8a8_quantize_act(int M, int K, const void* X, int ldx, svdq_out dtype, void* codes, float* scale,
+                              svdq_stream_t stream) {
+  return w8a8_quantize_impl(false, M, K, X, ldx, nullptr, 0, nullptr, 0.0f, nullptr, 0, dtype, codes, scale, stream);
+}
+
+svdq_status w8a8_rmsnorm_quantize(int M, int K, const void* X, int ldx, const void* residual, int ldr,
+                                  const void* weight, float eps, void* residual_out, int ldo, svdq_out dtype,
+                                  void* codes, float* scale, svdq_stream_t stream) {
+  return w8a8_quantize_impl(true, M, K, X, ldx, residual, ldr, weight, eps, residual_out, ldo, dtype, codes, scale,
+                            stream);
+}
+
+svdq_status w8a8_linear(int M, int N, int K, const void* a_codes, const float* a_scale, const void* w_codes,
+                        const float* w_scale, const void* bias, svdq_act act, const void* residual, int ldr,
+                        void* Y, int ldy, svdq_out out, svdq_stream_t stream) {
+  return w8a8_linear_impl(false, M, N, K, a_codes, a_scale, w_codes, w_scale, bias, act, residual, ldr, Y, ldy, out,
+                          stream);
+}
+
+svdq_status w8a8_gated_linear(int M, int F, int K, const void* a_codes, const float* a_scale, const void* w_codes,
+                              const float* w_scale, const void* bias, svdq_act act, void* Y, int ldy, svdq_out out,
+                              svdq_stream_t stream) {
+  return w8a8_linear_impl(true, M, F, K, a_codes, a_scale, w_codes, w_scale, bias, act, nullptr, 0, Y, ldy, out,
+                          stream);
+}
+
+svdq_status svdq_rope(int M, int heads, int head_dim, int pairs, int axes, const void* positions, int position_bytes,
+                      const double* freq, const int* axis, float scale, int interleaved, svdq_out dtype,
+                      const void* X, int ldx, int ldhx, void* Y, int ldy, int ldhy, svdq_stream_t stream) {
+  RopeParams p;
+  if (svdq_status st = rope_params(&p, M, axes, pairs, positions, position_bytes, freq, axis, scale); st != SVDQ_OK)
+    return st;
+  if (dtype != SVDQ_OUT_BF16 && dtype != SVDQ_OUT_F32) return SVDQ_ERR_INVALID_ARG;
+  if (heads < 1 || head_dim < 2 || head_dim % 2 || 2 * pairs > head_dim || !X || !Y) return SVDQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(heads) * head_dim > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
+  if (ldx < 0 || ldhx < 0 || ldx % 2 || ldhx % 2 || ldy % 2 || ldhy % 2) return SVDQ_ERR_INVALID_ARG;
+  // rows and heads of Y do not meet, in whichever order they lie
+  const long long row_span = (heads - 1ll) * ldhy + head_dim, head_span = (M - 1ll) * ldy + head_dim;
+  if (ldy < head_dim || ldhy < head_dim || (ldy < row_span && M > 1 && ldhy < head_span && heads > 1))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y)) return SVDQ_ERR_ALIGNMENT;
+  DeviceInfo* d = nullptr;
+  if (svdq_status st = device_setup(&d); st != SVDQ_OK) return st;
+  p.heads = heads;
+  p.D = head_dim;
+  p.X = X;
+  p.ldx = ldx;
+  p.ldhx = ldhx;
+  p.Y = Y;
+  p.ldy = ldy;
+  p.ldhy = ldhy;
+  // the widest vector (16 bytes at most) that every row, head and half starts on
+  const int all = ldx | ldhx | ldy | ldhy | head_dim | (interleaved ? 0 : pairs);
+  const bool f32 = dtype == SVDQ_OUT_F32;
+  int V = f32 ? 4 : 8;
+  while (all % V) V /= 2;
+  auto kern = f32 ? (V == 4 ? rope_kernel_of<float, 4>(interleaved)
+                            : (V == 2 ? rope_kernel_of<float, 2>(interleaved) : rope_kernel_of<float, 1>(interleaved)))
+                  : (V == 8   ? rope_kernel_of<__nv_bfloat16, 8>(interleaved)
+                     : V == 4 ? rope_kernel_of<__nv_bfloat16, 4>(interleaved)
+                     : V == 2 ? rope_kernel_of<__nv_bfloat16, 2>(interleaved)
+                              : rope_kernel_of<__nv_bfloat16, 1>(interleaved));
+  if (launch_kernel(d, kern, dim3(M), dim3(256), 0, static_cast<cudaStream_t>(stream), 1, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SVDQ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+svdq_status svdq_rope_table(int M, int pairs, int axes, const void* positions, int position_bytes, const double* freq,
+                            const int* axis, float scale, int angle_major, float* cos, float* sin,
+                            svdq_stream_t stream) {
+  RopeParams p;
+  if (svdq_status st = rope_params(&p, M, axes, pairs, positions, position_bytes, freq, axis, scale); st != SVDQ_OK)
+    return st;
+  if (!cos || !sin) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned4(cos) || !aligned4(sin)) return SVDQ_ERR_ALIGNMENT;
+  DeviceInfo* d = nullptr;
+  if (svdq_status st = device_setup(&d); st != SVDQ_OK) return st;
+  p.cos = cos;
+  p.sin = sin;
+  unsigned grid = grid_for(static_cast<size_t>(M) * pairs, 256);
+  if (grid > static_cast<unsigned>(8 * d->num_sms)) grid = 8 * d->num_sms;
+  if (launch_kernel(d, angle_major ? rope_table_kernel<true> : rope_table_kernel<false>, dim3(grid), dim3(256), 0,
+                    static_cast<cudaStream_t>(stream), 1, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SVDQ_ERR_CUDA;
+  }
   return launch_status();
 }
 

@@ -1,16 +1,19 @@
 """User-facing layers over the C ABI: the SVDQ W4A4 linear and the AWQ W4A16
 linear (the ``SVDQW4A4Linear`` / ``AWQW4A16Linear`` runtime layers of the
 Diffusers blog, "quantization_config"), with preallocated workspaces so a
-forward call is two (or one) library calls and no allocation."""
+forward call is two (or one) library calls and no allocation; the 8-bit linear
+and gated feed-forward block for layers that lose too much in four bits; and
+rotary positions."""
 
 from __future__ import annotations
 
 import torch
 
 from . import prep
-from . import (awq_w4a16_linear, svdq_codes_bytes, svdq_quantize_act, svdq_quantize_act_two_level,
-               svdq_scales_bytes, svdq_tensor_scale, svdq_w4a4_linear, svdq_w4a4_linear_qkv_norm_rope,
-               svdq_w4a4_linear_two_level, svdq_xl1_splits)
+from . import (awq_w4a16_linear, svdq_codes_bytes, svdq_quantize_act, svdq_quantize_act_two_level, svdq_rope,
+               svdq_rope_table, svdq_scales_bytes, svdq_tensor_scale, svdq_w4a4_linear, svdq_w4a4_linear_qkv_norm_rope,
+               svdq_w4a4_linear_two_level, svdq_xl1_splits, w8a8_gated_linear, w8a8_linear, w8a8_quantize_act,
+               w8a8_rmsnorm_quantize)
 
 
 class SvdqW4A4Linear:
@@ -122,8 +125,16 @@ class SvdqQkvNormRope(SvdqW4A4Linear):
 
     def forward(self, x: torch.Tensor, rope_cos: torch.Tensor | None = None,
                 rope_sin: torch.Tensor | None = None, y: torch.Tensor | None = None,
-                stream=None) -> torch.Tensor:
+                stream=None, rotary: "RotaryEmbedding | None" = None,
+                positions: torch.Tensor | None = None) -> torch.Tensor:
+        """The angle tables, or a rotary embedding and the rows' positions to make them of."""
         M = x.shape[0]
+        if rotary is not None or positions is not None:
+            if rope_cos is not None or rope_sin is not None or rotary is None or positions is None:
+                raise ValueError("give the tables, or a rotary embedding and positions")
+            if not rotary.interleaved or rotary.rot_dim != 128:
+                raise ValueError("the fused QKV projection turns adjacent pairs of whole 128-column heads")
+            rope_cos, rope_sin = rotary.tables(positions, angle_major=True, stream=stream)
         if M > self.max_tokens:
             raise ValueError(f"{M} tokens > workspace for {self.max_tokens}")
         xl1 = self.xl1[:svdq_xl1_splits(M, self.K, self.r) * M * self.r] if self.r else None
@@ -152,5 +163,117 @@ class AwqW4A16Linear:
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         return awq_w4a16_linear(x, self.w["qweight"], self.w["sz"], self.bias, self.w["N"], Y=y,
                                 stream=stream)
+
+    __call__ = forward
+
+
+class RotaryEmbedding:
+    """Rotary positions of heads: frequencies once (prep.rope_frequencies), then any rows'
+    heads turned, or the tables of their angles. ``dims`` is the number of rotary columns,
+    or one number per position axis; ``interleaved`` pairs adjacent columns, otherwise
+    column i pairs with column i + (rotary columns) / 2."""
+
+    def __init__(self, dims, base: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
+                 factor: float = 1.0, original_length: int | None = None, device="cuda"):
+        freq, axis, self.scale = prep.rope_frequencies(dims, base, scaling, factor, original_length)
+        self.rot_dim = 2 * freq.numel()
+        self.interleaved = bool(interleaved)
+        self.freq = freq.to(device)
+        # one axis: the library's default
+        self.axis = None if isinstance(dims, int) or len(dims) == 1 else axis.to(device)
+
+    def tables(self, positions: torch.Tensor, angle_major: bool = False, cos=None, sin=None, stream=None):
+        """(cos, sin) float32 [M, pairs], or [pairs, M] with angle_major (SvdqQkvNormRope's)."""
+        return svdq_rope_table(positions, self.freq, axis=self.axis, scale=self.scale, angle_major=angle_major,
+                               cos=cos, sin=sin, stream=stream)
+
+    def forward(self, x: torch.Tensor, positions: torch.Tensor, y: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+        """x [M, heads, D] turned; y may be x."""
+        return svdq_rope(x, positions, self.freq, axis=self.axis, scale=self.scale, interleaved=self.interleaved,
+                         Y=y, stream=stream)
+
+    __call__ = forward
+
+
+class W8A8Linear:
+    """Y = act(X W^T + bias) + residual with E4M3 rows of X and W (w8a8_quantize_act,
+    w8a8_linear)."""
+
+    def __init__(self, weights: dict, bias: torch.Tensor | None, max_tokens: int, activation: str | None = None):
+        self.w, self.bias, self.activation = weights, bias, activation
+        dev = weights["codes"].device
+        self.max_tokens = max_tokens
+        self.codes = torch.empty((max_tokens, weights["K"]), dtype=torch.float8_e4m3fn, device=dev)
+        self.scale = torch.empty(max_tokens, dtype=torch.float32, device=dev)
+
+    @classmethod
+    def from_linear(cls, weight: torch.Tensor, bias: torch.Tensor | None, max_tokens: int,
+                    activation: str | None = None):
+        """From an nn.Linear's weight [N, K] bf16 and bias [N] bf16 or None."""
+        return cls(prep.prepare_w8a8_weights(weight), bias, max_tokens, activation)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+        M = x.shape[0]
+        if M > self.max_tokens:
+            raise ValueError(f"{M} tokens > workspace for {self.max_tokens}")
+        codes, scale = w8a8_quantize_act(x, codes=self.codes[:M], scale=self.scale[:M], stream=stream)
+        return self.forward_quantized(codes, scale, residual, y, stream)
+
+    def forward_quantized(self, codes: torch.Tensor, scale: torch.Tensor, residual: torch.Tensor | None = None,
+                          y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The product alone, on rows quantized already (by a norm that feeds several layers, say)."""
+        return w8a8_linear(codes, scale, self.w["codes"], self.w["scale"], self.bias, residual=residual,
+                           activation=self.activation, Y=y, stream=stream)
+
+    __call__ = forward
+
+
+class W8A8GatedMlp:
+    """A pre-norm gated feed-forward block in 8 bits, on the residual stream:
+    h = x (+ residual);  out = h + down(act(gate(norm(h))) * up(norm(h))), four calls:
+    norm into E4M3, the gated product, its rows into E4M3, the second projection with h added in its
+    epilogue. ``up`` holds the F gate rows and then the F up rows [2F, K]; ``down`` [K, F]."""
+
+    def __init__(self, up: dict, down: dict, norm: torch.Tensor | None, max_tokens: int, activation: str = "silu",
+                 eps: float = 1e-6):
+        if up["N"] != 2 * down["K"] or up["K"] != down["N"]:
+            raise ValueError("up must be [2F, K] and down [K, F]")
+        self.up, self.down, self.norm = up, down, norm
+        self.activation, self.eps = activation, float(eps)
+        dev = up["codes"].device
+        K, F = up["K"], down["K"]
+        self.max_tokens = max_tokens
+        self.codes = torch.empty((max_tokens, K), dtype=torch.float8_e4m3fn, device=dev)
+        self.hidden = torch.empty((max_tokens, F), dtype=torch.bfloat16, device=dev)
+        self.hidden_codes = torch.empty((max_tokens, F), dtype=torch.float8_e4m3fn, device=dev)
+        self.scale = torch.empty((2, max_tokens), dtype=torch.float32, device=dev)
+
+    @classmethod
+    def from_linears(cls, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, norm: torch.Tensor | None,
+                     max_tokens: int, activation: str = "silu", eps: float = 1e-6):
+        """From the gate, up [F, K] and down [K, F] weights, bf16; norm [K] bf16 or None."""
+        if gate.shape != up.shape:
+            raise ValueError("gate and up must be equal [F, K] weights")
+        return cls(prep.prepare_w8a8_weights(torch.cat([gate, up])), prep.prepare_w8a8_weights(down), norm,
+                   max_tokens, activation, eps)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+        """x (and residual) [M, K] bf16 -> [M, K] bf16; with a residual, y (or a new tensor)
+        also holds h between the calls. y may be x or residual."""
+        M = x.shape[0]
+        if M > self.max_tokens:
+            raise ValueError(f"{M} tokens > workspace for {self.max_tokens}")
+        codes, scale, h = w8a8_rmsnorm_quantize(x, self.norm, residual, eps=self.eps, codes=self.codes[:M],
+                                                scale=self.scale[0, :M], residual_out=None if residual is None else y,
+                                                stream=stream)
+        hidden = w8a8_gated_linear(codes, scale, self.up["codes"], self.up["scale"], activation=self.activation,
+                                   Y=self.hidden[:M], stream=stream)
+        codes, scale = w8a8_quantize_act(hidden, codes=self.hidden_codes[:M], scale=self.scale[1, :M], stream=stream)
+        h = x if h is None else h
+        return w8a8_linear(codes, scale, self.down["codes"], self.down["scale"], residual=h,
+                           Y=h if residual is not None else y, stream=stream)
 
     __call__ = forward

@@ -16,10 +16,13 @@ would produce a checkpoint.
 
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import (awq_quantize_weight, svdq_lowrank_factors, svdq_pack_lowrank, svdq_quantize_act,
-               svdq_quantize_act_two_level, svdq_residual, svdq_smoothing, svdq_tensor_scale)
+               svdq_quantize_act_two_level, svdq_residual, svdq_smoothing, svdq_tensor_scale,
+               w8a8_quantize_act)
 
 
 def smoothing(x_absmax: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
@@ -72,3 +75,54 @@ def prepare_awq_weights(w: torch.Tensor) -> dict:
     N, K = w.shape
     qt, szt = awq_quantize_weight(w.contiguous())
     return {"qweight": qt, "sz": szt, "N": N, "K": K}
+
+
+def prepare_w8a8_weights(w: torch.Tensor) -> dict:
+    """w [N, K] bf16 or float32 -> E4M3 rows and their float32 scales (w8a8_quantize_act)."""
+    N, K = w.shape
+    codes, scale = w8a8_quantize_act(w.contiguous())
+    return {"codes": codes, "scale": scale, "N": N, "K": K}
+
+
+def rope_frequencies(dims, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_length: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """What svdq_rope takes besides the positions: (freq float64 [P], axis int32 [P], scale).
+
+    ``dims``: the rotary columns of a head, one even number, or one for each position
+    axis (for images, say frame, row and column). Within an axis of d columns pair i
+    turns by base^(-2i/d) radians per position. For contexts longer than the trained
+    one, ``scaling``:
+
+    * "linear": every frequency divided by ``factor``;
+    * "ntk": the base times factor^(d/(d-2)), which leaves the fastest pair as it is and
+      divides the slowest by ``factor``;
+    * "yarn": by how often a pair turns within ``original_length`` positions: pairs that
+      turn more than beta_fast times stay, those below beta_slow are divided by
+      ``factor``, a ramp over the pair's index between; cosine and sine are multiplied
+      by 0.1 ln(factor) + 1.
+    """
+    dims = (dims,) if isinstance(dims, int) else tuple(dims)
+    if not dims or any(d < 2 or d % 2 for d in dims):
+        raise ValueError("dims must be even numbers of columns")
+    if scaling not in (None, "linear", "ntk", "yarn") or not factor >= 1.0 or not base > 1.0:
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn', factor at least 1, base above 1")
+    if scaling == "yarn" and not original_length:
+        raise ValueError("yarn needs original_length")
+    if scaling == "ntk" and 2 in dims and factor != 1.0:
+        raise ValueError("ntk needs more than one pair per axis")
+    freqs, axes = [], []
+    for a, d in enumerate(dims):
+        i = torch.arange(d // 2, dtype=torch.float64)
+        f = (base * factor ** (d / (d - 2)) if scaling == "ntk" and d > 2 else base) ** (-2.0 * i / d)
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            # the (real) index of the pair that turns `turns` times within the original length
+            at = lambda turns: d * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
+            low, high = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), d - 1)
+            ramp = ((i - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
+            f = f / factor * ramp + f * (1.0 - ramp)
+        freqs.append(f)
+        axes.append(torch.full((d // 2,), a, dtype=torch.int32))
+    scale = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
+    return torch.cat(freqs), torch.cat(axes), scale

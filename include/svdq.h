@@ -17,6 +17,9 @@
  * (svdq_tensor_scale, svdq_quantize_act_two_level, svdq_w4a4_linear_two_level),
  * the fused QKV projection with head norm and rotation
  * (svdq_w4a4_linear_qkv_norm_rope), the fused MLP's fc1 (svdq_mlp_fc1), the AWQ W4A16 linear (awq_w4a16_linear),
+ * the 8-bit linear for layers that four bits cost too much (w8a8_quantize_act,
+ * w8a8_rmsnorm_quantize, w8a8_linear, w8a8_gated_linear), rotary positions
+ * (svdq_rope, svdq_rope_table),
  * layout conversion (svdq_pack, svdq_unpack, svdq_pack_lowrank), offline weight
  * preparation (svdq_column_absmax, svdq_smoothing, svdq_lowrank_factors,
  * svdq_residual, awq_quantize_weight), buffer sizes, and the device status word
@@ -35,7 +38,8 @@
  *    status word, read (and cleared) by svdq_check_device_status; the outputs
  *    of every call enqueued since the previous check are then undefined.
  *  - Matrices are row-major. bf16/fp16 are IEEE-style 16-bit patterns.
- *  - Shapes: M >= 1; K % 64 == 0; N % 16 == 0; r == 0 or (r % 16 == 0 and r <= 256).
+ *  - Shapes: M >= 1; K % 64 == 0 (w8a8_*: K % 16 == 0); N % 16 == 0; r == 0 or
+ *    (r % 16 == 0 and r <= 256).
  */
 #ifndef SVDQ_H_
 #define SVDQ_H_
@@ -64,6 +68,9 @@ typedef enum {
 } svdq_format;
 
 typedef enum { SVDQ_OUT_BF16 = 0, SVDQ_OUT_F32 = 1 } svdq_out;
+
+/* the activation of an epilogue: none, GELU (tanh form), SiLU */
+typedef enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU = 1, SVDQ_ACT_SILU = 2 } svdq_act;
 
 typedef enum {
   SVDQ_PACK_ACT = 0,    /* activation codes + scales */
@@ -441,6 +448,95 @@ svdq_status svdq_residual(int N, int K, int r, const void* W, const float* smoot
                           const void* L2, void* R, svdq_stream_t stream);
 svdq_status awq_quantize_weight(int N, int K, const void* W, void* qweight, void* sz,
                                 svdq_stream_t stream);
+
+/*
+ * The 8-bit linear: E4M3 codes (sign, 4 exponent bits, 3 fraction bits, largest
+ * value 448), one float32 scale per activation row and one per weight row, for the
+ * layers of a model that lose too much in four bits. Codes are plain row-major
+ * bytes [rows, K], K % 16 == 0; a weight [N, K] is quantized by
+ * w8a8_quantize_act(N, K, ...) like an activation. X, residual and Y are bf16 or
+ * float32 (`dtype` / `out`), row-major with a row stride in elements, rows on
+ * 16-byte boundaries.
+ *
+ * w8a8_quantize_act -- each row to codes and a scale:
+ *   t = max(max_k |X[m,k]|, 2^-100),  scale[m] = RN32(t / 448),
+ *   codes[m,k] = RN_e4m3(X[m,k] * RN32(448 / t))
+ * An all-zero row has codes 0. A row that holds NaN or infinity has a scale that
+ * is not finite, and so has every output of the products that read it; other
+ * rows are not touched by it.
+ *   X [M, ldx], ldx >= K;  codes [M, K] bytes, 16-byte aligned, written;
+ *   scale float32 [M], written;  16 <= K <= 32768.
+ *
+ * w8a8_rmsnorm_quantize -- the residual's addition and a root-mean-square norm in
+ * front of it, in the same pass over the row:
+ *   h = X + residual (float32),  residual_out = RN(h),
+ *   y = h / sqrt(mean_k(h^2) + eps) * weight,  then as above on y
+ * The norm reads h before its rounding to residual_out.
+ *   residual, residual_out  [M, ldr], [M, ldo] like X, both or neither (h = X);
+ *                           residual_out may be residual or X itself
+ *   weight                  bf16 [K], 16-byte aligned, or NULL (1)
+ *   eps                     finite, >= 0
+ *
+ * w8a8_linear -- the product with its epilogue:
+ *   Y[m,n] = act((sum_k a[m,k] w[n,k]) a_scale[m] w_scale[n] + bias[n]) + residual[m,n]
+ * float32 sums, one rounding to Y's type at the end.
+ *   a_codes [M, K], a_scale [M], w_codes [N, K], w_scale [N]
+ *   bias      bf16 [N] or NULL
+ *   residual  [M, ldr] of Y's type or NULL; may be Y itself (with ldr == ldy)
+ *   Y         [M, ldy], written;  N % 16 == 0
+ *
+ * w8a8_gated_linear -- the first half of a gated feed-forward block, both
+ * projections and the product in one kernel; the weight holds F gate rows, then F
+ * up rows:
+ *   z as above (without residual) for n < 2F,  Y[m,n] = act(z[m,n]) * z[m,F+n]
+ *   w_codes [2F, K], w_scale [2F], bias bf16 [2F] or NULL, Y [M, ldy >= F];  F % 16 == 0
+ *
+ * INVALID_ARG / ALIGNMENT on bad arguments, before any launch.
+ */
+svdq_status w8a8_quantize_act(int M, int K, const void* X, int ldx, svdq_out dtype, void* codes, float* scale,
+                              svdq_stream_t stream);
+svdq_status w8a8_rmsnorm_quantize(int M, int K, const void* X, int ldx, const void* residual, int ldr,
+                                  const void* weight, float eps, void* residual_out, int ldo, svdq_out dtype,
+                                  void* codes, float* scale, svdq_stream_t stream);
+svdq_status w8a8_linear(int M, int N, int K, const void* a_codes, const float* a_scale, const void* w_codes,
+                        const float* w_scale, const void* bias, svdq_act act, const void* residual, int ldr,
+                        void* Y, int ldy, svdq_out out, svdq_stream_t stream);
+svdq_status w8a8_gated_linear(int M, int F, int K, const void* a_codes, const float* a_scale, const void* w_codes,
+                              const float* w_scale, const void* bias, svdq_act act, void* Y, int ldy, svdq_out out,
+                              svdq_stream_t stream);
+
+/*
+ * Rotary positions. Pair i of a head turns by angle(m, i) = positions[m, axis[i]] *
+ * freq[i]; c = scale cos(angle), s = scale sin(angle); (a, b) -> (a c - b s, b c + a s).
+ *
+ * positions  [M, axes] int32 or int64 (position_bytes 4 or 8), any value
+ * freq       float64 [pairs], radians per position: the base's powers, with whatever
+ *            scaling a longer context asks for already in them
+ * axis       int32 [pairs], the position axis of each pair (0 <= axis < axes; any
+ *            other value gives NaN in that pair), or NULL: axis 0 for all
+ * scale      factor on both tables (1, or a longer context's attention factor), finite
+ * The angles are formed in 64 bits, so positions may be far: an angle is off by 2^-52
+ * of itself and 2^-64 turns per position before its cosine is rounded to float32.
+ *
+ * svdq_rope -- turns the heads of every row:
+ *   X, Y  [M, heads, head_dim] bf16 or float32, 16-byte aligned, head_dim contiguous;
+ *         element (m, h, j) at m ld + h ldh + j (either order of rows and heads: Q and
+ *         K inside a [M, 3 H D] projection, or [heads, M, head_dim]); ld, ldh even; Y may
+ *         be X itself with the same strides, and otherwise overlaps nothing
+ *   interleaved  pairs are columns (2i, 2i + 1); else (i, i + pairs)
+ *   columns from 2 pairs on are copied;  head_dim even, 2 pairs <= head_dim, pairs <= 512.
+ *
+ * svdq_rope_table -- the tables alone: cos, sin float32 [M, pairs], or [pairs, M] with
+ * angle_major (the layout svdq_w4a4_linear_qkv_norm_rope takes, with pairs = 64).
+ *
+ * INVALID_ARG / ALIGNMENT on bad arguments, before any launch.
+ */
+svdq_status svdq_rope(int M, int heads, int head_dim, int pairs, int axes, const void* positions, int position_bytes,
+                      const double* freq, const int* axis, float scale, int interleaved, svdq_out dtype,
+                      const void* X, int ldx, int ldhx, void* Y, int ldy, int ldhy, svdq_stream_t stream);
+svdq_status svdq_rope_table(int M, int pairs, int axes, const void* positions, int position_bytes, const double* freq,
+                            const int* axis, float scale, int angle_major, float* cos, float* sin,
+                            svdq_stream_t stream);
 
 /*
  * svdq_check_device_status -- synchronises `stream`, then reads and clears the

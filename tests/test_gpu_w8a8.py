@@ -1,0 +1,348 @@
+"""The 8-bit linear path on the GPU against the float64 oracle: the row quantizer bit for bit,
+the norm in front of it, the product and its epilogue, the gated product, and a block of
+them together. Each bound counts the roundings of the arithmetic it covers.
+
+U = 2^-24 is half a float32 step, H the output type's half step (finfo.eps / 2)."""
+
+import numpy as np
+import pytest
+
+from oracle import w8a8 as O
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+U = 2.0 ** -24
+TYPES = pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+
+
+@pytest.fixture(scope="module")
+def bq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import bit_quantized_diffusion_b200 as bq
+    return bq
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def draw(seed, *shape, dtype=F32, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).cuda()
+
+
+def inside(t, cols, fill):
+    """t in the middle columns of a wider tensor full of `fill`: (the view, the whole)."""
+    whole = torch.full((t.shape[0], t.shape[1] + 2 * cols), fill, dtype=t.dtype, device=t.device)
+    whole[:, cols: cols + t.shape[1]] = t
+    return whole[:, cols: cols + t.shape[1]], whole
+
+
+def outer_is(whole, cols, fill):
+    return bool((whole[:, :cols] == fill).all() and (whole[:, whole.shape[1] - cols:] == fill).all())
+
+
+# ------------------------------------------------------------------ quantizer
+@TYPES
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 3840), (3, 48), (7, 1040), (130, 512), (33, 4112), (2, 15360), (2, 32768)])
+def test_quantize_rows_bit_for_bit(bq, M, K, dtype):
+    x = draw(M + K, M, K, dtype=dtype)
+    x *= torch.logspace(-20, 20, M, device="cuda").to(dtype)[:, None] if M > 1 else 1
+    x[:, K // 2] *= 30
+    codes, scale = bq.w8a8_quantize_act(x)
+    want, want_scale = O.quantize_rows(f64(x))
+    assert np.array_equal(f64(scale), want_scale) and np.array_equal(f64(codes), want)
+
+
+@TYPES
+def test_quantize_rows_at_the_edges(bq, dtype):
+    x = torch.zeros(9, 64, dtype=dtype)
+    x[1, 5] = -0.0
+    x[2, 3] = 2.0 ** -126                      # below the floor
+    x[3] = torch.linspace(-1, 1, 64) * 2.0 ** -99
+    x[4] = torch.linspace(-1, 1, 64) * 3e38
+    x[5] = -2.5
+    x[6, 7], x[7, 8], x[8, 9] = float("nan"), float("inf"), float("-inf")
+    x[6:, 0] = 3.0
+    codes, scale = bq.w8a8_quantize_act(x.cuda())
+    want, want_scale = O.quantize_rows(f64(x[:6]))
+    assert np.array_equal(f64(codes)[:6], want) and np.array_equal(f64(scale)[:6], want_scale)
+    assert torch.isnan(scale[6]) and torch.isinf(scale[7]) and torch.isinf(scale[8])
+    # a strided input gives the same as a packed one, and codes go where they are told
+    view, _ = inside(x.cuda(), 16, float("nan"))
+    buf = torch.full((9, 64), 1.0, device="cuda").to(E4)
+    c2, s2 = bq.w8a8_quantize_act(view, codes=buf)
+    assert c2 is buf and torch.equal(c2.view(torch.uint8), codes.view(torch.uint8))
+    assert torch.equal(s2[:6], scale[:6])
+
+
+# ------------------------------------------------------------------ norm
+def norm_bounds(x, w, r, eps, K):
+    """h is one rounding; the sum of squares of K values in float32, added by threads in a
+    chain of at most 32 and trees of 5 + 5: 42 roundings and one per square; a square root
+    halves that, and five more roundings lead to y: in all below 40 U of y."""
+    h, y = O.rmsnorm(f64(x), None if w is None else f64(w), None if r is None else f64(r), eps)
+    return h, y, 40 * U
+
+
+def check_norm(codes, scale, y, rel):
+    t = np.maximum(np.abs(y).max(1), O.FLOOR)
+    s, c = f64(scale), f64(codes)
+    assert np.all(np.abs(s - t / 448) <= (rel + 2 * U) * t / 448)
+    # half a step of E4M3: 2^-4 of the value, 2^-10 below the smallest normal
+    err = np.abs(c * s[:, None] - y)
+    assert np.all(err <= np.abs(y) * (2.0 ** -4 + 3 * rel) + s[:, None] * 2.0 ** -10 * (1 + 3 * rel))
+
+
+@TYPES
+@pytest.mark.parametrize("M,K,weight,residual", [
+    (1, 16, True, False), (1, 3840, True, True), (5, 48, False, True), (64, 1040, True, True), (3, 15360, True, True),
+    (2, 32768, False, False), (300, 512, True, True)])
+def test_rmsnorm_quantize(bq, M, K, weight, residual, dtype):
+    x, w = draw(1, M, K, dtype=dtype), (1 + draw(2, K, std=0.2)).to(BF) if weight else None
+    x[:, 3] *= 40
+    r = draw(3, M, K, dtype=dtype, std=3.0) if residual else None
+    codes, scale, out = bq.w8a8_rmsnorm_quantize(x, w, r, eps=1e-5)
+    h, y, rel = norm_bounds(x, w, r, 1e-5, K)
+    check_norm(codes, scale, y, rel)
+    if not residual:
+        assert out is None
+        return
+    assert out.dtype == dtype and np.all(np.abs(f64(out) - h) <= half_step(dtype) * np.abs(h) + U * np.abs(h))
+    # in place on the residual stream, inside wider rows whose other columns stay
+    rv, whole = inside(r, 8, 7.0)
+    xv, _ = inside(x, 16, float("nan"))
+    c2, s2, o2 = bq.w8a8_rmsnorm_quantize(xv, w, rv, eps=1e-5, residual_out=rv)
+    assert o2 is rv and torch.equal(rv, out) and outer_is(whole, 8, 7.0)
+    assert torch.equal(c2.view(torch.uint8), codes.view(torch.uint8)) and torch.equal(s2, scale)
+
+
+def test_rmsnorm_rows_of_their_own(bq):
+    """Zero rows, tiny rows, and rows that are not finite, which touch no other."""
+    x = draw(4, 6, 64)
+    clean = bq.w8a8_rmsnorm_quantize(x)
+    x[1], x[2], x[3, 5], x[4, 6] = 0.0, x[2] * 1e-30, float("nan"), float("inf")
+    codes, scale, _ = bq.w8a8_rmsnorm_quantize(x)
+    assert torch.isfinite(scale[:3]).all() and not f64(codes)[1].any() and not torch.isfinite(scale[3:5]).any()
+    for row in (0, 5):
+        assert torch.equal(codes[row].view(torch.uint8), clean[0][row].view(torch.uint8))
+        assert scale[row] == clean[1][row]
+    y = f64(x)[2:3] / np.sqrt(1e-6)
+    check_norm(codes[2:3], scale[2:3], y, 40 * U)
+
+
+# ------------------------------------------------------------------ product
+def operands(bq, M, rows, K, seed):
+    x = draw(seed, M, K)
+    x[:, K // 3] *= 30
+    return (*bq.w8a8_quantize_act(x), *bq.w8a8_quantize_act(draw(seed + 1, rows, K, std=0.02)))
+
+
+def product_bound(a, sa, w, sw, bias, K):
+    """(z, its error): a matrix instruction adds 32 products to the running sum; allow each such
+    step 2^-22 of the magnitudes' sum (products aligned to the largest, then cut), splits and
+    joins of K a few more, and the epilogue four roundings."""
+    z, mag = O.product(f64(a), f64(sa), f64(w), f64(sw), None if bias is None else f64(bias))
+    return z, mag * ((K / 32 + 16) * 2.0 ** -22 + 4 * U)
+
+
+def act_bound(z, ez, kind):
+    """|gelu'|, |silu'| < 1.13; evaluated through exp(e) and a quotient: exp's relative error is
+    its argument's rounding |e| U and a few U of its own, the quotient two, damped by
+    exp/(1 + exp) < 1: (|e| + 12) U of the value, |e| <= 40 wherever the value counts."""
+    if kind is None:
+        return z, ez
+    return O.act(z, kind), 1.13 * ez + 64 * U * np.abs(O.act(z, kind)) + 1e-15
+
+
+CASES = [  # M, N, K, bias, act, residual
+    (1, 16, 16, False, None, False), (1, 3840, 512, True, None, True), (2, 48, 4096, True, "silu", True),
+    (7, 1040, 784, False, "gelu", False), (16, 272, 3856, True, None, False), (17, 128, 144, True, "gelu", True),
+    (33, 528, 1040, True, None, True), (64, 256, 2048, False, "silu", True), (65, 2064, 272, True, None, True),
+    (128, 400, 8192, True, "gelu", True), (129, 144, 640, True, None, False), (255, 768, 320, False, None, True),
+    (257, 272, 128, True, "silu", True), (300, 1552, 656, True, None, True), (700, 512, 1536, True, "gelu", True),
+    (1100, 528, 112, True, None, True)]
+
+
+@TYPES
+@pytest.mark.parametrize("M,N,K,bias,act,residual", CASES)
+def test_linear(bq, M, N, K, bias, act, residual, dtype):
+    a, sa, w, sw = operands(bq, M, N, K, 10 * M + N)
+    b = draw(5, N, dtype=BF, std=0.1) if bias else None
+    r = draw(6, M, N, dtype=dtype) if residual else None
+    z, ez = product_bound(a, sa, w, sw, b, K)
+    want, e = act_bound(z, ez, act)
+    if residual:
+        want, e = want + f64(r), e + U * np.abs(want)
+    y = bq.w8a8_linear(a, sa, w, sw, b, residual=r, activation=act, out_dtype=dtype)
+    err = np.abs(f64(y) - want)
+    assert np.all(err <= e * 1.01 + (half_step(dtype) + 2 * U) * (np.abs(want) + e)), (err - e).max()
+    # inside wider rows, whose other columns stay; the residual strided, and in place
+    yv, whole = inside(torch.zeros_like(y), 16, 5.0)
+    if residual:
+        yv.copy_(r)
+    got = bq.w8a8_linear(a, sa, w, sw, b, residual=yv if residual else None, activation=act, out_dtype=dtype, Y=yv)
+    assert got is yv and torch.equal(yv, y) and outer_is(whole, 16, 5.0)
+    assert bq.svdq_check_device_status() == 0
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 40, 128, 200, 384])
+def test_linear_is_exact_on_whole_numbers(bq, M):
+    """Small whole numbers and scales of powers of two: every sum is exact in float32, in any order."""
+    K, N = 2064, 208
+    g = torch.Generator().manual_seed(M)
+    a = torch.randint(-8, 9, (M, K), generator=g).float()
+    w = torch.randint(-8, 9, (N, K), generator=g).float()
+    sa, sw = 2.0 ** torch.randint(-3, 4, (M,), generator=g).float(), 2.0 ** torch.randint(-3, 4, (N,), generator=g).float()
+    b, r = torch.randint(-9, 10, (N,), generator=g).to(BF), torch.randint(-9, 10, (M, N), generator=g).float()
+    y = bq.w8a8_linear(a.to(E4).cuda(), sa.cuda(), w.to(E4).cuda(), sw.cuda(), b.cuda(), residual=r.cuda(), out_dtype=F32)
+    want = (a.double() @ w.double().t()) * sa.double()[:, None] * sw.double() + b.double() + r.double()
+    assert torch.equal(y.cpu().double(), want)
+
+
+@TYPES
+@pytest.mark.parametrize("M,F,K,bias,act", [
+    (1, 16, 16, False, "silu"), (1, 1040, 3840, False, "silu"), (4, 272, 1040, True, "silu"), (16, 64, 4112, True, "gelu"),
+    (31, 400, 144, False, "silu"), (64, 528, 2048, True, None), (128, 80, 512, False, "gelu"), (130, 272, 656, True, "silu"),
+    (300, 464, 384, True, "gelu"), (600, 1040, 256, False, "silu")])
+def test_gated_linear(bq, M, F, K, bias, act, dtype):
+    a, sa, w, sw = operands(bq, M, 2 * F, K, M + F)
+    b = draw(5, 2 * F, dtype=BF, std=0.1) if bias else None
+    z, ez = product_bound(a, sa, w, sw, b, K)
+    gate, eg = act_bound(z[:, :F], ez[:, :F], act)
+    up, eu = z[:, F:], ez[:, F:]
+    want, e = gate * up, np.abs(gate) * eu + np.abs(up) * eg + eg * eu
+    y = bq.w8a8_gated_linear(a, sa, w, sw, b, activation=act, out_dtype=dtype)
+    assert np.all(np.abs(f64(y) - want) <= e * 1.01 + (half_step(dtype) + 2 * U) * (np.abs(want) + e))
+    yv, whole = inside(torch.zeros_like(y), 8, 5.0)
+    bq.w8a8_gated_linear(a, sa, w, sw, b, activation=act, out_dtype=dtype, Y=yv)
+    assert torch.equal(yv, y) and outer_is(whole, 8, 5.0)
+    assert bq.svdq_check_device_status() == 0
+
+
+@pytest.mark.parametrize("M", [3, 20, 150, 300])
+def test_a_row_that_is_not_finite_touches_no_other(bq, M):
+    N = K = 160
+    a, sa, w, sw = operands(bq, M, N, K, M)
+    clean = bq.w8a8_linear(a, sa, w, sw, out_dtype=F32)
+    gated = bq.w8a8_gated_linear(a, sa, w, sw, out_dtype=F32)
+    sa[1], sw[2] = float("nan"), float("inf")
+    a.view(torch.uint8)[2, 5] = 0x7F                        # an E4M3 NaN
+    y = bq.w8a8_linear(a, sa, w, sw, out_dtype=F32)
+    u = bq.w8a8_gated_linear(a, sa, w, sw, out_dtype=F32)
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2]).all() and not torch.isfinite(y[:, 2]).any()
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[1:3] = False
+    assert torch.equal(y[keep][:, 3:], clean[keep][:, 3:]) and torch.equal(u[keep][:, 3:], gated[keep][:, 3:])
+
+
+def test_activations_far_out(bq):
+    """+-inf-sized and far arguments keep the activations' limits."""
+    a = torch.full((1, 16), 1.0, device="cuda").to(E4)
+    w = torch.zeros(16, 16, device="cuda")
+    w[:8, 0] = torch.tensor([448.0, -448.0, 100.0, -100.0, 10.0, -10.0, 0.0, -0.0625])
+    sw = torch.ones(16, device="cuda")
+    for scale in (1.0, 1e9, 1e30):
+        sa = torch.full((1,), scale, device="cuda")
+        z = f64(w.to(E4)[:, 0]) * float(sa)
+        for act in ("silu", "gelu"):
+            y = f64(bq.w8a8_linear(a, sa, w.to(E4), sw, activation=act, out_dtype=F32))[0]
+            want = O.act(z, act)
+            assert np.all(np.isfinite(y)) and np.all(np.abs(y - want) <= 64 * U * np.abs(want) + 1e-30 * scale)
+
+
+# ------------------------------------------------------------------ use
+@pytest.mark.parametrize("M", [1, 24, 200])
+def test_graphs_streams_and_repeats(bq, M):
+    """Captured and replayed on other inputs, two graphs in turn, on a stream of its own, and
+    twice the same: all the bits of the plain call."""
+    N, K = 272, 1040
+    x, r = draw(1, M, K, dtype=BF), draw(2, M, K, dtype=BF)
+    w, sw = bq.w8a8_quantize_act(draw(3, N, K, std=0.02))
+    g, sg = bq.w8a8_quantize_act(draw(4, 2 * N, K, std=0.02))
+
+    def once(x, r):
+        codes, scale, h = bq.w8a8_rmsnorm_quantize(x, None, r)
+        return h, bq.w8a8_linear(codes, scale, w, sw), bq.w8a8_gated_linear(codes, scale, g, sg)
+
+    want = once(x, r)
+    again = once(x, r)
+    other = once(x * 2, r)
+    for t, u in zip(want, again):
+        assert torch.equal(t, u)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    codes, scale, h = bq.w8a8_rmsnorm_quantize(x, None, r, stream=side)
+    y = bq.w8a8_linear(codes, scale, w, sw, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(h, want[0]) and torch.equal(y, want[1])
+    sx, sr = x.clone(), r.clone()
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(once(sx, sr))
+        graphs.append(graph)
+    sx.copy_(x * 2)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        for t, u in zip(out, other):
+            assert torch.equal(t, u)
+    assert bq.svdq_check_device_status() == 0
+
+
+@pytest.mark.parametrize("M", [1, 50, 300])
+def test_gated_block_together(bq, M):
+    """W8A8GatedMlp and W8A8Linear: the block against its parts in float64, the 8-bit
+    rounding of the hidden rows included through the kernels' own codes."""
+    from bit_quantized_diffusion_b200.layers import W8A8GatedMlp, W8A8Linear
+    K, F = 512, 1040
+    gate, up = draw(1, F, K, dtype=BF, std=0.04), draw(2, F, K, dtype=BF, std=0.04)
+    down, norm = draw(3, K, F, dtype=BF, std=0.03), (1 + draw(4, K, std=0.1)).to(BF)
+    x, r = draw(5, M, K, dtype=BF), draw(6, M, K, dtype=BF, std=2.0)
+    block = W8A8GatedMlp.from_linears(gate, up, down, norm, max_tokens=M + 3)
+    y = block(x, r)
+    h, n, _ = norm_bounds(x, norm, r, 1e-6, K)
+    check_norm(block.codes[:M], block.scale[0, :M], n, 40 * U)
+    z, ez = product_bound(block.codes[:M], block.scale[0, :M], block.up["codes"], block.up["scale"], None, K)
+    g, eg = act_bound(z[:, :F], ez[:, :F], "silu")
+    hidden, e = g * z[:, F:], np.abs(g) * ez[:, F:] + np.abs(z[:, F:]) * eg
+    assert np.all(np.abs(f64(block.hidden[:M]) - hidden) <= 1.01 * e + (2.0 ** -8 + 2 * U) * (np.abs(hidden) + e))
+    codes, scale = O.quantize_rows(f64(block.hidden[:M]))
+    assert np.array_equal(f64(block.hidden_codes[:M]), codes) and np.array_equal(f64(block.scale[1, :M]), scale)
+    z, ez = product_bound(block.hidden_codes[:M], block.scale[1, :M], block.down["codes"], block.down["scale"], None, F)
+    # h itself went through bf16 on its way to the second projection
+    want, e = z + h, ez + 2.0 ** -8 * np.abs(h)
+    assert np.all(np.abs(f64(y) - want) <= 1.01 * e + (2.0 ** -8 + 4 * U) * (np.abs(want) + e))
+    # in place on the residual stream, without a residual, and the plain layer with its epilogue
+    rr = r.clone()
+    assert block(x, rr, y=rr) is rr and torch.equal(rr, y)
+    hb = h.astype(np.float32)
+    same = block(torch.from_numpy(hb).cuda().to(BF))
+    assert torch.allclose(same.float(), y.float(), rtol=0, atol=0.25 * float(y.float().abs().max()))
+    lin = W8A8Linear.from_linear(gate, None, max_tokens=M, activation="gelu")
+    out = lin(x)
+    z, ez = product_bound(lin.codes[:M], lin.scale[:M], lin.w["codes"], lin.w["scale"], None, K)
+    want, e = act_bound(z, ez, "gelu")
+    assert np.all(np.abs(f64(out) - want) <= 1.01 * e + (2.0 ** -8 + 2 * U) * (np.abs(want) + e))
+    assert bq.svdq_check_device_status() == 0
+
+
+def test_other_device_is_refused(bq):
+    if torch.cuda.device_count() < 2:
+        x = torch.zeros(4, 64, dtype=BF)
+        with pytest.raises(ValueError, match="CUDA"):
+            bq.w8a8_quantize_act(x, codes=torch.zeros(4, 64, device="cuda").to(E4))
+        return
+    with pytest.raises(ValueError, match="current device"):
+        bq.w8a8_quantize_act(torch.zeros(4, 64, dtype=BF, device="cuda:1"))
