@@ -142,7 +142,15 @@ svdq_status device_setup(DeviceInfo** out) {
         cudaFuncSetAttribute(w8a8_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kW8SmemBytes)) != cudaSuccess ||
         cudaFuncSetAttribute(w8a8_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kW8SmemBytes)) != cudaSuccess)
+                             static_cast<int>(kW8SmemBytes)) != cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_stream_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_stream_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_stream_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_stream_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) !=
+            cudaSuccess)
       return SVDQ_ERR_CUDA;
     // all of the SM's unified L1/shared storage as shared memory, so that the
     // occupancy the host code plans for (e.g. two quantizer CTAs per SM) is real
@@ -157,6 +165,10 @@ svdq_status device_setup(DeviceInfo** out) {
                           reinterpret_cast<const void*>(w4a4_mlp_fc1_kernel),
                           reinterpret_cast<const void*>(w8a8_gemm_kernel<false>),
                           reinterpret_cast<const void*>(w8a8_gemm_kernel<true>),
+                          reinterpret_cast<const void*>(w8a8_stream_kernel<false, false>),
+                          reinterpret_cast<const void*>(w8a8_stream_kernel<false, true>),
+                          reinterpret_cast<const void*>(w8a8_stream_kernel<true, false>),
+                          reinterpret_cast<const void*>(w8a8_stream_kernel<true, true>),
                           reinterpret_cast<const void*>(awq_gemv_kernel<1>),
                           reinterpret_cast<const void*>(awq_gemv_kernel<2>)})
       if (cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -1087,6 +1099,55 @@ svdq_status awq_quantize_weight(int N, int K, const void* W, void* qweight, void
 
 namespace {
 
+// The 8-bit linear of at most kWsMaxT tokens: one cluster of `splits` CTAs per tile of
+// 128 weight rows, the smallest power of two (at most 8, at most half the K tiles) that
+// gives four in five SMs a CTA (77 tokens, K = 3840: N = 3840 takes 14.7, 11.1, 9.2, 10.9 us
+// with 1, 2, 4, 8; N = 15360 17.7, 17.7, 23.9). More CTAs than SMs share them two by two.
+svdq_status launch_w8a8_stream(const DeviceInfo* d, bool gated, const W8Params& q, const void* a_codes,
+                               const void* w_codes, void* Y, int ldy, svdq_stream_t stream) {
+  WsParams p;
+  p.M = q.M;
+  p.N = q.N;
+  p.K = q.K;
+  p.T = (q.M + 15) / 16 * 16;
+  p.tb = p.T <= 32 ? 32 : (p.T <= 64 ? 64 : 128);
+  const int tile_n = gated ? 64 : 128, tiles = (q.N + tile_n - 1) / tile_n;
+  const int ktiles = (q.K + kW8KStage - 1) / kW8KStage;
+  if (tiles > INT32_MAX / 8) return SVDQ_ERR_UNSUPPORTED;
+  int splits = 1;
+  while (splits < 8 && 2 * splits <= ktiles && 5ll * tiles * splits < 4ll * d->num_sms) splits *= 2;
+  p.splits = splits;
+  const size_t budget = tiles * splits > d->num_sms ? 113 * 1024 : 226 * 1024;
+  const int per_cta = (ktiles + splits - 1) / splits;
+  int stages = kWsMaxStages;
+  while (stages > 2 && (ws_smem_bytes(p.T, stages) > budget || stages > per_cta)) --stages;
+  p.stages = stages;
+  p.act = q.act;
+  p.out_f32 = q.out_f32;
+  p.a_scale = q.a_scale;
+  p.w_scale = q.w_scale;
+  p.bias = q.bias;
+  p.residual = q.residual;
+  p.ldr = q.ldr;
+  p.Y = Y;
+  p.ldy = ldy;
+  p.status = q.status;
+  CUtensorMap tm_w, tm_x;
+  if (!make_tmap_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, q.K, gated ? 2ull * q.N : q.N, q.K, kW8KStage, 64,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, q.K, q.M, q.K, kW8KStage, p.T,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+    return SVDQ_ERR_CUDA;
+  auto kern = gated ? (splits > 1 ? w8a8_stream_kernel<true, true> : w8a8_stream_kernel<true, false>)
+                    : (splits > 1 ? w8a8_stream_kernel<false, true> : w8a8_stream_kernel<false, false>);
+  if (launch_kernel(d, kern, dim3(tiles * splits), dim3(kWsThreads), ws_smem_bytes(p.T, stages),
+                    static_cast<cudaStream_t>(stream), splits, tm_w, tm_x, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SVDQ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
 // the 8-bit linear and its gated form (N: output columns; gated, the weight has 2 N rows)
 svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_codes, const float* a_scale,
                              const void* w_codes, const float* w_scale, const void* bias, svdq_act act,
@@ -1104,34 +1165,61 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
     return SVDQ_ERR_ALIGNMENT;
   DeviceInfo* d = nullptr;
   if (svdq_status st = device_setup(&d); st != SVDQ_OK) return st;
-  CUtensorMap tm_a, tm_b, tm_y;
-  const bool f32 = out == SVDQ_OUT_F32;
-  if (!make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, K, M, K, kW8KStage, kW8BM,
-                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, K, gated ? 2ull * N : N, K, kW8KStage,
-                    kW8BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      // output: 32 x 32 boxes, bf16 rows of 64 B (64-byte swizzle) or f32 rows of 128 B
-      !make_tmap_2d(&tm_y, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M,
-                    ldy * esz, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-    return SVDQ_ERR_CUDA;
   W8Params p;
   p.M = M;
   p.N = N;
   p.K = K;
-  const int tile_n = gated ? kW8BN / 2 : kW8BN;
-  const long long tiles_m = (static_cast<long long>(M) + 2 * kW8BM - 1) / (2 * kW8BM);
-  const long long tiles = tiles_m * ((static_cast<long long>(N) + tile_n - 1) / tile_n);
-  if (tiles > INT32_MAX / 2) return SVDQ_ERR_UNSUPPORTED;
-  p.tiles_m = static_cast<int>(tiles_m);
-  p.tiles = static_cast<int>(tiles);
   p.act = act == SVDQ_ACT_GELU ? kW8ActGelu : (act == SVDQ_ACT_SILU ? kW8ActSilu : kW8ActNone);
-  p.out_f32 = f32;
+  p.out_f32 = out == SVDQ_OUT_F32;
   p.a_scale = a_scale;
   p.w_scale = w_scale;
   p.bias = static_cast<const __nv_bfloat16*>(bias);
   p.residual = residual;
   p.ldr = ldr;
   p.status = d->status;
+  // Few tokens stream the weight (K = 3840, N = 15360 at 64 / 128 / 256 tokens: 16.5 / 20.1
+  // / 32.0 us against 20.3 / 21.7 / 23.3 in CTA pairs); above 64 only where K is long enough
+  // to hide the wider sum at its end (K = N = 1024 at 64 / 128: 5.0 / 6.6 against 5.2 / 5.2).
+  if (M <= 64 || (M <= kWsMaxT && K >= 2048)) return launch_w8a8_stream(d, gated, p, a_codes, w_codes, Y, ldy, stream);
+  // The tile's width: the one whose waves of tiles over the CTA pairs take least, a stage
+  // of K costing its operands' way in, 256 + bn rows per pair (at 256 columns that equals its
+  // MMA time). K = 3840: M = 256, N = 3840 takes 10.7 us at 64 columns and 18.4 at 256, M = 4608
+  // 101 and 65; of 28 shapes measured at every width the choice was the fastest each time.
+  const long long tiles_m = (static_cast<long long>(M) + 2 * kW8BM - 1) / (2 * kW8BM);
+  long long best = -1;
+  for (int bn = kW8MaxBN; bn >= 64; bn -= gated ? 64 : 32) {
+    const int tile_n = gated ? bn / 2 : bn;
+    const long long tiles = tiles_m * ((static_cast<long long>(N) + tile_n - 1) / tile_n);
+    const long long waves = (tiles + d->w8_pairs - 1) / d->w8_pairs;
+    const long long cost = waves * (bn + 256);
+    if (tiles <= INT32_MAX / 2 && (best < 0 || cost < best)) {
+      best = cost;
+      p.bn = bn;
+      p.tiles = static_cast<int>(tiles);
+    }
+  }
+  if (best < 0) return SVDQ_ERR_UNSUPPORTED;
+  p.tiles_m = static_cast<int>(tiles_m);
+  // Row tiles in bands whose rows of A stay in a part of L2 while the weight passes by:
+  // the weight is read once per band, A once. (M, K, N) = (4096, 15360, 3840), A 63 MB: two
+  // bands 211 us, one 219; (4608, 3840, 2 x 10240), A 18 MB: one band 280 us, two 287.
+  long long band = (40ll << 20) / (2ll * kW8BM * K);
+  if (band < 1) band = 1;
+  const long long bands = (tiles_m + band - 1) / band;
+  p.band = static_cast<int>((tiles_m + bands - 1) / bands);
+  p.band_tiles = p.band * (p.tiles / p.tiles_m);
+  p.stages = static_cast<int>(kW8Ring / (kW8AStage + p.bn / 2 * kW8KStage));
+  if (p.stages > kW8MaxStages) p.stages = kW8MaxStages;
+  CUtensorMap tm_a, tm_b, tm_y;
+  const bool f32 = out == SVDQ_OUT_F32;
+  if (!make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, K, M, K, kW8KStage, kW8BM,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, K, gated ? 2ull * N : N, K, kW8KStage,
+                    p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      // output: 32 x 32 boxes, bf16 rows of 64 B (64-byte swizzle) or f32 rows of 128 B
+      !make_tmap_2d(&tm_y, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M,
+                    ldy * esz, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return SVDQ_ERR_CUDA;
   const int units = p.tiles < d->w8_pairs ? p.tiles : d->w8_pairs;
   auto kern = gated ? w8a8_gemm_kernel<true> : w8a8_gemm_kernel<false>;
   if (launch_kernel(d, kern, dim3(units * 2), dim3(kW8Threads), kW8SmemBytes, static_cast<cudaStream_t>(stream), 2,

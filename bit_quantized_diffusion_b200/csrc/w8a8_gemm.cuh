@@ -10,10 +10,10 @@
 // float32 and the epilogue applies both scales once per output; nothing but Y is
 // rounded to 16 bits, once.
 //
-// w8a8_gemm_kernel: persistent, a cluster of two CTAs on two SMs per 256 x 256 tile
-// (cta_group::2): each CTA stages its own 128 rows of A and 128 of the tile's B rows
-// (128 bytes of K per row and stage, 128-byte swizzle). A gated tile takes 128 gate
-// rows in the first CTA and the matching 128 up rows in the second, so both halves
+// w8a8_gemm_kernel: persistent, a cluster of two CTAs on two SMs per 256 x bn tile
+// (cta_group::2): each CTA stages its own 128 rows of A and half of the tile's bn B rows
+// (128 bytes of K per row and stage, 128-byte swizzle). A gated tile takes bn / 2 gate
+// rows in the first CTA and the matching bn / 2 up rows in the second, so both halves
 // of an output meet in one accumulator and the [M, 2F] product never reaches memory.
 // K need not fill the last stage: TMA fills both operands with zeros there.
 //
@@ -21,7 +21,7 @@
 //   warp 0     TMA producer
 //   warp 1     tensor-memory owner; in the leader CTA also the MMA issuer (one thread)
 //   warps 2-9  epilogue, two warps per tensor-memory lane quadrant
-// Tensor memory holds two 256-column accumulators, so a tile's epilogue runs under
+// Tensor memory holds two accumulators of up to 256 columns, so a tile's epilogue runs under
 // the next tile's MMAs.
 #pragma once
 
@@ -32,17 +32,16 @@ namespace svdq {
 constexpr int kW8Threads = 320;
 constexpr int kW8EpiWarps = 8;
 constexpr int kW8BM = 128;                      // rows per CTA (a pair's tile: 256)
-constexpr int kW8BN = 256;                      // accumulator columns per tile
+constexpr int kW8MaxBN = 256;                   // accumulator columns per tile, at most
 constexpr int kW8KStage = 128;                  // values (bytes) of K per stage
-constexpr int kW8Stages = 5;
 constexpr int kW8AStage = kW8BM * kW8KStage;    // 16 KB
-constexpr int kW8BStage = (kW8BN / 2) * kW8KStage;
-constexpr int kW8StageBytes = kW8AStage + kW8BStage;
 constexpr int kW8StageOut = 4096;               // epilogue staging bytes per warp
-constexpr uint32_t kW8Out = kW8Stages * kW8StageBytes;
+constexpr uint32_t kW8Ring = 5 * (kW8AStage + kW8MaxBN / 2 * kW8KStage);  // 160 KB of stages
+constexpr int kW8MaxStages = 8;
+constexpr uint32_t kW8Out = kW8Ring;
 constexpr uint32_t kW8Vec = kW8Out + kW8EpiWarps * kW8StageOut;  // per warp: scales [128], bias [128]
 constexpr uint32_t kW8Bars = kW8Vec + kW8EpiWarps * 256 * 4;
-constexpr uint32_t kW8TmemSlot = kW8Bars + 8 * (2 * kW8Stages + 4);
+constexpr uint32_t kW8TmemSlot = kW8Bars + 8 * (2 * kW8MaxStages + 4);
 constexpr size_t kW8SmemBytes = kW8TmemSlot + 16 + 1024;
 static_assert(kW8SmemBytes <= 232448, "shared memory of one CTA");
 
@@ -50,7 +49,10 @@ enum W8Act : int { kW8ActNone = 0, kW8ActGelu = 1, kW8ActSilu = 2 };
 
 struct W8Params {
   int M, N, K;                 // N: output columns (F when gated)
+  int bn;                      // accumulator columns per tile: a multiple of 32, gated of 64
+  int stages;                  // ring stages of bn's size
   int tiles_m, tiles;
+  int band, band_tiles;        // tiles run through bands of this many row tiles, M fastest within
   int act;
   int out_f32;
   const float* a_scale;        // [M]
@@ -91,8 +93,9 @@ template <bool kGated>
 __global__ void __launch_bounds__(kW8Threads, 1)
     w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_y, const W8Params p) {
-  constexpr int NS = kW8Stages;
-  constexpr int kTileN = kGated ? kW8BN / 2 : kW8BN;  // output columns per tile
+  const int NS = p.stages, half_n = p.bn / 2;
+  const int tile_n = kGated ? half_n : p.bn;  // output columns per tile
+  const uint32_t stage_bytes = kW8AStage + static_cast<uint32_t>(half_n) * kW8KStage;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -105,10 +108,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   const int my_tiles = p.tiles > unit ? (p.tiles - 1 - unit) / units + 1 : 0;
   auto tile_mn = [&](int i, int& m0, int& n0) {
     const int t = unit + i * units;
-    m0 = (t % p.tiles_m) * (2 * kW8BM);
-    n0 = (t / p.tiles_m) * kTileN;
+    const int band = t / p.band_tiles, r = t - band * p.band_tiles;
+    const int rows = min(p.band, p.tiles_m - band * p.band);
+    m0 = (band * p.band + r % rows) * (2 * kW8BM);
+    n0 = r / rows * tile_n;
   };
-  auto a_st = [&](int s) { return sbase + s * kW8StageBytes; };
+  auto a_st = [&](int s) { return sbase + s * stage_bytes; };
   auto b_st = [&](int s) { return a_st(s) + kW8AStage; };
   auto bar_full = [&](int s) { return sbase + kW8Bars + 8 * s; };
   auto bar_empty = [&](int s) { return sbase + kW8Bars + 8 * (NS + s); };
@@ -145,55 +150,55 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   if (warp == 0) {
     if (elect_one()) {
       bool ok = true;
-      int g = 0;
+      int s = 0, phase = 0;  // ring stage, and the parity of its use
       for (int i = 0; i < my_tiles && ok; ++i) {
         int m0, n0;
         tile_mn(i, m0, n0);
         const int mrow = m0 + kW8BM * static_cast<int>(rank);
-        const int nrow = kGated ? n0 + (leader ? 0 : p.N) : n0 + kW8BN / 2 * static_cast<int>(rank);
-        for (int kt = 0; kt < ktiles; ++kt, ++g) {
-          const int s = g % NS;
-          ok = mbar_wait(bar_empty(s), ((g / NS) & 1) ^ 1, p.status);
+        const int nrow = n0 + (leader ? 0 : (kGated ? p.N : half_n));
+        for (int kt = 0; kt < ktiles; ++kt) {
+          ok = mbar_wait(bar_empty(s), phase ^ 1, p.status);
           if (!ok) break;
-          if (leader) mbar_arrive_expect_tx(bar_full(s), 2 * kW8StageBytes);
+          if (leader) mbar_arrive_expect_tx(bar_full(s), 2 * stage_bytes);
           const uint32_t fb = lead(bar_full(s));
           tma_load_2d_pair(a_st(s), &tm_a, fb, kt * kW8KStage, mrow);
           tma_load_2d_pair(b_st(s), &tm_b, fb, kt * kW8KStage, nrow);
+          if (++s == NS) s = 0, phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
     if (leader && elect_one()) {
       bool ok = true;
-      constexpr uint32_t id = idesc_e4m3_f32(2 * kW8BM, kW8BN);
+      const uint32_t id = idesc_e4m3_f32(2 * kW8BM, p.bn);
       const uint64_t a0 = smem_desc(a_st(0), 16, 1024, kSwizzle128B);
       const uint64_t b0 = smem_desc(b_st(0), 16, 1024, kSwizzle128B);
-      constexpr uint64_t kStep = static_cast<uint64_t>(kW8StageBytes >> 4);
-      int g = 0;
+      const uint64_t step = static_cast<uint64_t>(stage_bytes >> 4);
+      int s = 0, phase = 0;
       for (int i = 0; i < my_tiles && ok; ++i) {
-        const uint32_t acc = tmem + (i & 1) * kW8BN;
+        const uint32_t acc = tmem + (i & 1) * kW8MaxBN;
         if (i >= 2) {  // both CTAs' epilogues have read this accumulator
           ok = mbar_wait(bar_acc_free(i & 1), ((i >> 1) - 1) & 1, p.status);
           if (!ok) break;
         }
         tc_fence_after();
-        for (int kt = 0; kt < ktiles; ++kt, ++g) {
-          const int s = g % NS;
-          ok = mbar_wait(bar_full(s), (g / NS) & 1, p.status);
+        for (int kt = 0; kt < ktiles; ++kt) {
+          ok = mbar_wait(bar_full(s), phase, p.status);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t ad = a0 + kStep * static_cast<uint64_t>(s), bd = b0 + kStep * static_cast<uint64_t>(s);
+          const uint64_t ad = a0 + step * static_cast<uint64_t>(s), bd = b0 + step * static_cast<uint64_t>(s);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 values of K per MMA, 32 bytes (2 units) further along the row
             mma_f8_pair(acc, ad + 2 * k, bd + 2 * k, id, (kt > 0 || k > 0) ? 1u : 0u);
           tc_commit_pair(bar_empty(s), 0x3);
+          if (++s == NS) s = 0, phase ^= 1;
         }
         if (ok) tc_commit_pair(bar_acc_full(i & 1), 0x3);
       }
     }
   } else {
     const int quad = warp & 3;         // tensor-memory lanes 32 quad .. 32 quad + 31
-    const int half = (warp - 2) >> 2;  // which of the quadrant's two warps
+    const int half = (warp - 2) >> 2;  // which of the quadrant's two warps: it takes every other sub-tile
     const int ew = warp - 2;
     const uint32_t out_buf = sbase + kW8Out + ew * kW8StageOut;
     float* sw_s = reinterpret_cast<float*>(smem + kW8Vec) + ew * 256;  // [4 sub-tiles][32]
@@ -206,15 +211,13 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       const int mrow = m0 + kW8BM * static_cast<int>(rank) + quad * 32;
       const int m = mrow + lane;
       const float sa = m < p.M ? p.a_scale[m] : 0.0f;
-      // this warp's accumulator columns: sub-tile t starts at col(t); output column n0 + ocol(t)
-      auto col = [&](int t) { return kGated ? (t & 1) * 128 + (half * 2 + (t >> 1)) * 32 : half * 128 + t * 32; };
+      // scales and bias of this warp's 32-column sub-tiles; gated, the up rows' 64 further on
       __syncwarp();
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        // the weight row of this column
-        const int oc = n0 + (kGated ? (col(t) & 127) : col(t)) + lane;
+        const int oc = n0 + (2 * (kGated ? t & 1 : t) + half) * 32 + lane;
         const bool in = oc < p.N;
-        const int row = kGated && (t & 1) ? p.N + oc : oc;
+        const int row = kGated && t >= 2 ? p.N + oc : oc;
         sw_s[t * 32 + lane] = in ? p.w_scale[row] : 0.0f;
         bias_s[t * 32 + lane] = in && p.bias != nullptr ? __bfloat162float(p.bias[row]) : 0.0f;
       }
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t t_row = tmem + (i & 1) * kW8BN + (static_cast<uint32_t>(quad * 32) << 16);
+      const uint32_t t_row = tmem + (i & 1) * kW8MaxBN + (static_cast<uint32_t>(quad * 32) << 16);
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -302,40 +305,31 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         }
         ++stores;
       };
-      if constexpr (kGated) {
+      const int subs = tile_n / 32;  // the tile's sub-tiles; this warp's: half, half + 2, ...
+      if (half >= subs) release();
 #pragma unroll 1
-        for (int t = 0; t < 4; t += 2) {
-          uint32_t ga[32], ua[32];
-          tmem_ld32(t_row + col(t), ga);
-          tmem_ld32(t_row + col(t + 1), ua);
-          tmem_ld_wait();
-          if (t == 2) release();
-          const int n = n0 + col(t);
-          if (n >= p.N || mrow >= p.M) continue;  // warp-uniform
-          float y[32], u[32];
-          finish(ga, t, y);
-          finish(ua, t + 1, u);
+      for (int t = half; t < subs; t += 2) {
+        uint32_t acc[32];
+        tmem_ld32(t_row + t * 32, acc);
+        uint32_t up[kGated ? 32 : 1];
+        if constexpr (kGated) tmem_ld32(t_row + half_n + t * 32, up);
+        tmem_ld_wait();
+        if (t + 2 >= subs) release();
+        const int n = n0 + t * 32;
+        if (n >= p.N || mrow >= p.M) continue;  // warp-uniform
+        float y[32];
+        finish(acc, t >> 1, y);
+        if (p.act != kW8ActNone) {
 #pragma unroll
-          for (int q = 0; q < 32; ++q) y[q] = w8_act(y[q], p.act) * u[q];
-          store_sub(y, n);
+          for (int q = 0; q < 32; ++q) y[q] = w8_act(y[q], p.act);
         }
-      } else {
-#pragma unroll 1
-        for (int t = 0; t < 4; ++t) {
-          uint32_t acc[32];
-          tmem_ld32(t_row + col(t), acc);
-          tmem_ld_wait();
-          if (t == 3) release();
-          const int n = n0 + col(t);
-          if (n >= p.N || mrow >= p.M) continue;  // warp-uniform
-          float y[32];
-          finish(acc, t, y);
-          if (p.act != kW8ActNone) {
+        if constexpr (kGated) {
+          float u[32];
+          finish(up, 2 + (t >> 1), u);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) y[q] = w8_act(y[q], p.act);
-          }
-          store_sub(y, n);
+          for (int q = 0; q < 32; ++q) y[q] *= u[q];
         }
+        store_sub(y, n);
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -349,6 +343,263 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+}
+
+// w8a8_stream_kernel: up to 128 tokens, where the product is bound by reading the
+// weight once. The operands change sides: 128 weight rows are the MMA's M (tensor-memory
+// lanes), the tokens, rounded up to 16, its N, so a handful of tokens costs no padding
+// to 256 rows. One tile of 128 weight rows (gated: 64 gate rows and the 64 matching up
+// rows) per cluster, whose CTAs split K and add their float32 partial sums through
+// distributed shared memory, in rank order: weights narrower than a row tile per SM
+// still keep every SM loading, without memory to add in and without atomics.
+//
+//   warp 0     TMA producer: W [2 x 64 rows x 128 B] and X [T x 128 B] per stage
+//   warp 1     tensor-memory owner and MMA issuer (one thread)
+//   warps 2-9  the residual's lines into L2; then accumulator -> shared memory [T][128],
+//              two warps per tensor-memory lane quadrant
+//   all warps  the sum over the cluster and the epilogue, four adjacent outputs per
+//              thread and step, a thread's columns the same in every step
+constexpr int kWsThreads = 320;
+constexpr int kWsMaxT = 128;
+constexpr int kWsMaxStages = 12;
+
+struct WsParams {
+  int M, N, K;                 // N: output columns (F when gated)
+  int T, tb;                   // tokens rounded up to 16; tensor-memory columns (32, 64, 128)
+  int splits, stages;          // cluster size; pipeline stages
+  int act, out_f32;
+  const float* a_scale;
+  const float* w_scale;
+  const __nv_bfloat16* bias;
+  const void* residual;
+  size_t ldr;
+  void* Y;
+  size_t ldy;
+  uint32_t* status;
+};
+
+__host__ __device__ constexpr uint32_t ws_stage_bytes(int T) { return 128 * 128 + static_cast<uint32_t>(T) * 128; }
+constexpr uint32_t kWsTail = 8 * (2 * kWsMaxStages + 1) + 24;  // barriers, tensor-memory slot
+__host__ __device__ constexpr size_t ws_smem_bytes(int T, int stages) {
+  return static_cast<size_t>(stages) * ws_stage_bytes(T) + kWsTail + 1024;
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float4 lds_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+// four adjacent values of the output's type
+__device__ __forceinline__ void w8_load4(const void* base, size_t at, int f32, float (&r)[4]) {
+  if (f32) {
+    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + at);
+    r[0] = __uint_as_float(v.x << 16); r[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    r[2] = __uint_as_float(v.y << 16); r[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void w8_store4(void* base, size_t at, int f32, const float (&y)[4]) {
+  if (f32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(y[0], y[1], y[2], y[3]);
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+template <bool kGated, bool kSplit>
+__global__ void __launch_bounds__(kWsThreads, 2)
+    w8a8_stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                       const WsParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int NS = p.stages, T = p.T;
+  const uint32_t SB = ws_stage_bytes(T);
+  const uint32_t bars = sbase + NS * SB;
+  auto bar_full = [&](int s) { return bars + 8 * s; };
+  auto bar_empty = [&](int s) { return bars + 8 * (NS + s); };
+  const uint32_t bar_acc = bars + 8 * 2 * NS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + NS * SB + 8 * (2 * NS + 1));
+  const int splits = kSplit ? p.splits : 1;
+  const int rank = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = blockIdx.x / splits;
+  constexpr int kCols = kGated ? 64 : 128;      // output columns per tile
+  const int n0 = tile * kCols;
+  const int ktiles = (p.K + kW8KStage - 1) / kW8KStage;
+  const int k0 = rank * ktiles / splits, k1 = (rank + 1) * ktiles / splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    mbar_init(bar_acc, 1);
+    fence_barrier_init();
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), p.tb);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cta_sync_converged();
+  grid_dep_wait();
+  grid_dep_launch();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // this CTA's share of the tile's outputs: items of four adjacent columns, e .. e1 in
+  // steps of the block, which keep a thread at the same columns; their scales and bias now
+  constexpr int kQuads = kCols / 4, kStep = kSplit ? 1 : (kGated ? 2 : 4);
+  static_assert(kWsThreads % kQuads == 0, "a thread keeps its columns");
+  const int items = p.M * kQuads;
+  const int e1 = (rank + 1) * items / splits;
+  int e = rank * items / splits + static_cast<int>(threadIdx.x);
+  const int c = 4 * (e % kQuads), n = n0 + c;
+  float sw[kGated ? 8 : 4], bias[kGated ? 8 : 4];
+#pragma unroll
+  for (int q = 0; q < (kGated ? 8 : 4); ++q) {
+    const int row = (q < 4 ? n : p.N + n) + (q & 3);
+    sw[q] = n < p.N ? p.w_scale[row] : 0.0f;
+    bias[q] = n < p.N && p.bias != nullptr ? __bfloat162float(p.bias[row]) : 0.0f;
+  }
+  // the cluster's four sums of row m from accumulator column col, in rank order
+  auto sum4 = [&](int m, int col) {
+    const uint32_t at = sbase + (m * 128 + col) * 4;
+    if (!kSplit) return lds_f4(at);
+    float4 v = lds_cluster_f4(map_peer_smem(at, 0));
+#pragma unroll 4
+    for (int r = 1; r < splits; ++r) {
+      const float4 o = lds_cluster_f4(map_peer_smem(at, r));
+      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+    }
+    return v;
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int kt = k0; kt < k1; ++kt) {
+        const int g = kt - k0, s = g % NS;
+        if (!mbar_wait(bar_empty(s), ((g / NS) & 1) ^ 1, p.status)) break;
+        const uint32_t st = sbase + s * SB;
+        mbar_arrive_expect_tx(bar_full(s), SB);
+        tma_load_2d(st, &tm_w, bar_full(s), kt * kW8KStage, n0);
+        tma_load_2d(st + 64 * 128, &tm_w, bar_full(s), kt * kW8KStage, kGated ? p.N + n0 : n0 + 64);
+        tma_load_2d(st + 128 * 128, &tm_x, bar_full(s), kt * kW8KStage, 0);
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      const uint32_t id = idesc_e4m3_f32(128, T);
+      bool ok = true;
+      for (int kt = k0; kt < k1; ++kt) {
+        const int g = kt - k0, s = g % NS;
+        ok = mbar_wait(bar_full(s), (g / NS) & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = sbase + s * SB;
+        const uint64_t wd = smem_desc(st, 16, 1024, kSwizzle128B);
+        const uint64_t xd = smem_desc(st + 128 * 128, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f8(tmem, wd + 2 * k, xd + 2 * k, id, (g > 0 || k > 0) ? 1u : 0u);
+        tc_commit(bar_empty(s));
+      }
+      if (ok) tc_commit(bar_acc);
+    }
+  } else {
+    const int quad = warp & 3;
+    if (p.residual != nullptr) {
+      // read at the very end, from memory it would add a full latency per step
+      const int esz = p.out_f32 ? 4 : 2, lines = kCols * esz / 128;
+      for (int i = threadIdx.x - 64; i < p.M * lines; i += kWsThreads - 64) {
+        const int col = n0 + (i % lines) * (128 / esz);
+        if (col < p.N)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p.residual) +
+                                                        (static_cast<size_t>(i / lines) * p.ldr + col) * esz));
+      }
+    }
+    // the stages' memory is free once the last MMA is done
+    bool ok = mbar_wait(bar_acc, 0, p.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      float* part = reinterpret_cast<float*>(smem);  // [T][128]
+      for (int c = (warp - 2) / 4 * 32; c < T; c += 64) {
+        uint32_t acc[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, acc);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 32; ++q)
+          if (c + q < T) part[(c + q) * 128 + quad * 32 + lane] = __uint_as_float(acc[q]);
+      }
+      tc_fence_before();
+    }
+  }
+  if (kSplit) cluster_sync_converged(); else cta_sync_converged();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tb);
+  }
+  if (n < p.N) {
+    for (; e < e1; e += kStep * kWsThreads) {
+      float r[kStep][4], sa[kStep];
+      float4 v[kStep], w[kStep];
+      // the step's loads together
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        const int m = (e + j * kWsThreads) / kQuads;
+        if (e + j * kWsThreads < e1) {
+          sa[j] = p.a_scale[m];
+          if (p.residual != nullptr) w8_load4(p.residual, static_cast<size_t>(m) * p.ldr + n, p.out_f32, r[j]);
+          v[j] = sum4(m, c);
+          if (kGated) w[j] = sum4(m, 64 + c);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        const int m = (e + j * kWsThreads) / kQuads;
+        if (e + j * kWsThreads < e1) {
+          float y[4] = {fmaf(v[j].x * sa[j], sw[0], bias[0]), fmaf(v[j].y * sa[j], sw[1], bias[1]),
+                        fmaf(v[j].z * sa[j], sw[2], bias[2]), fmaf(v[j].w * sa[j], sw[3], bias[3])};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = w8_act(y[q], p.act);
+          if (kGated) {
+            y[0] *= fmaf(w[j].x * sa[j], sw[4], bias[4]);
+            y[1] *= fmaf(w[j].y * sa[j], sw[5], bias[5]);
+            y[2] *= fmaf(w[j].z * sa[j], sw[6], bias[6]);
+            y[3] *= fmaf(w[j].w * sa[j], sw[7], bias[7]);
+          }
+          if (p.residual != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] += r[j][q];
+          }
+          w8_store4(p.Y, static_cast<size_t>(m) * p.ldy + n, p.out_f32, y);
+        }
+      }
+    }
+  }
+  // peers read this CTA's sums until here
+  if (kSplit) cluster_sync_converged();
 }
 
 }  // namespace svdq
