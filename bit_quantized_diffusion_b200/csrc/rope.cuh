@@ -8,10 +8,12 @@
 // Far positions: a float32 product position * freq is off by half a unit in its last
 // place, 0.03 radians at 10^6. The angle is formed in whole turns instead, freq / 2 pi
 // as a 64-bit binary fraction: position times that fraction modulo 2^64 is the angle's
-// fraction of a turn, the wrap of the integer product being the range reduction. Its
-// top 32 bits, as a signed number of turns in [-1/2, 1/2), go to sincospi. The
+// fraction of a turn, the wrap of the integer product being the range reduction. The
 // fraction carries freq's 53 bits down to 2^-64 of a turn: the angle is off by 2^-52 of
-// itself and 2^-64 turns per position.
+// itself and 2^-64 turns per position. Its top 32 bits are kept: the nearest quarter
+// turn, which swaps and signs, and a rest of at most an eighth either way, whose sine and
+// cosine are the first terms of their power series in float32 (x^9 and x^10; the terms
+// left out are below 2^-29).
 #pragma once
 
 #include "sm100.cuh"
@@ -45,105 +47,309 @@ __device__ __forceinline__ uint64_t rope_fraction(double freq) {
   return __double2ull_rd(part * 18446744073709551616.0);
 }
 
-__device__ __forceinline__ float2 rope_cos_sin(long long pos, uint64_t fraction, float scale) {
-  const uint64_t turn = static_cast<uint64_t>(pos) * fraction;
-  const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
-  float s, c;
-  sincospif(half_turns, &s, &c);
-  return make_float2(c * scale, s * scale);
+// The position's angle under a pair's fraction, in 2^-32 of a turn.
+__device__ __forceinline__ uint32_t rope_turn(long long pos, uint64_t fraction) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(pos) * fraction) >> 32);
+}
+
+// Cosines and sines of two angles, each times its scale: c = (c0, c1), s = (s0, s1). Both
+// angles go through the series together, as pairs of float32.
+__device__ __forceinline__ void rope_cos_sin2(uint32_t turn0, uint32_t turn1, float2 scale, float2& c, float2& s) {
+  // an eighth on: bits 31, 30 are the nearest quarter turn, the others the rest plus an eighth
+  const uint32_t t0 = turn0 + 0x20000000u, t1 = turn1 + 0x20000000u;
+  auto rest = [](uint32_t t) { return static_cast<float>(static_cast<int>(t & 0x3FFFFFFFu) - 0x20000000); };
+  auto k = [](float v) { return make_float2(v, v); };
+  const float2 x = __fmul2_rn(make_float2(rest(t0), rest(t1)), k(1.4629180792671596e-9f));  // 2 pi 2^-32
+  const float2 xx = __fmul2_rn(x, x);
+  float2 a = __ffma2_rn(xx, k(2.7557319e-6f), k(-1.9841270e-4f));   // 1 / 9!, 1 / 7!
+  a = __ffma2_rn(xx, a, k(8.3333333e-3f));                          // 1 / 5!
+  a = __ffma2_rn(xx, a, k(-1.6666667e-1f));                         // 1 / 3!
+  a = __ffma2_rn(__fmul2_rn(x, xx), a, x);
+  float2 b = __ffma2_rn(xx, k(-2.7557319e-7f), k(2.4801587e-5f));   // 1 / 10!, 1 / 8!
+  b = __ffma2_rn(xx, b, k(-1.3888889e-3f));                         // 1 / 6!
+  b = __ffma2_rn(xx, b, k(4.1666667e-2f));                          // 1 / 4!
+  b = __ffma2_rn(xx, b, k(-0.5f));
+  b = __ffma2_rn(xx, b, k(1.0f));
+  // each quarter turn on: (c, s) -> (-s, c)
+  auto turned = [](uint32_t t, float cv, float sv, float& co, float& so) {
+    const bool swap = t & 0x40000000u;
+    co = __uint_as_float(__float_as_uint(swap ? sv : cv) ^ ((t + 0x40000000u) & 0x80000000u));
+    so = __uint_as_float(__float_as_uint(swap ? cv : sv) ^ (t & 0x80000000u));
+  };
+  turned(t0, b.x, a.x, c.x, s.x);
+  turned(t1, b.y, a.y, c.y, s.y);
+  c = __fmul2_rn(c, scale);
+  s = __fmul2_rn(s, scale);
 }
 
 __device__ __forceinline__ long long rope_position(const RopeParams& p, size_t m, int axis) {
   const size_t at = m * p.A + axis;
-  return p.pos64 ? static_cast<const long long*>(p.positions)[at]
-                 : static_cast<long long>(static_cast<const int*>(p.positions)[at]);
+  return p.pos64 ? __ldg(static_cast<const long long*>(p.positions) + at)
+                 : static_cast<long long>(__ldg(static_cast<const int*>(p.positions) + at));
 }
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) RopeVec {
   T e[V];
 };
-__device__ __forceinline__ float rope_f(float v) { return v; }
-__device__ __forceinline__ float rope_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void rope_put(float& d, float v) { d = v; }
-__device__ __forceinline__ void rope_put(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
-
-// One block per (row, share of the heads). Its angles first, one per thread, into shared
-// memory; then units of V adjacent elements (half layout: V of the first and V of the
-// second half) over all its heads.
-template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
-  __shared__ float2 cs[kRopeMaxPairs];
-  const size_t m = blockIdx.x;
-  grid_dep_wait();
-  grid_dep_launch();
-  for (int i = threadIdx.x; i < p.P; i += blockDim.x) {
-    const int a = p.axis != nullptr ? p.axis[i] : 0;
-    // an axis that the positions do not have gives NaN, and no read
-    cs[i] = a >= 0 && a < p.A ? rope_cos_sin(rope_position(p, m, a), rope_fraction(p.freq[i]), p.scale)
-                              : make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+// V elements as float32 and back; bf16 two at a time
+template <int V>
+__device__ __forceinline__ void rope_unpack(const RopeVec<float, V>& v, float (&f)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] = v.e[j];
+}
+template <int V>
+__device__ __forceinline__ void rope_unpack(const RopeVec<__nv_bfloat16, V>& v, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = __bfloat162float(v.e[0]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[j / 2];
+      f[j] = __uint_as_float(w << 16);
+      f[j + 1] = __uint_as_float(w & 0xFFFF0000u);
+    }
   }
-  __syncthreads();
-  const T* x = static_cast<const T*>(p.X) + m * p.ldx;
-  T* y = static_cast<T*>(p.Y) + m * p.ldy;
-  const int R = 2 * p.P;
-  using Vec = RopeVec<T, V>;
-  // a head's units: interleaved, its V-element vectors; half layout, first those that hold
-  // pairs, then the copied ones
-  const int turned = p.P / V;
-  const int units = kInterleaved ? p.D / V : turned + (p.D - R) / V;
-  const int total = units * p.heads;
-  for (int u = blockIdx.y * blockDim.x + threadIdx.x; u < total; u += blockDim.x * gridDim.y) {
-    const int h = u / units, c = u % units;
-    const T* xh = x + static_cast<size_t>(h) * p.ldhx;
-    T* yh = y + static_cast<size_t>(h) * p.ldhy;
-    if (kInterleaved) {
-      Vec v = *reinterpret_cast<const Vec*>(xh + c * V);
+}
+template <int V>
+__device__ __forceinline__ void rope_pack(const float (&f)[V], RopeVec<float, V>& v) {
 #pragma unroll
-      for (int j = 0; j < V; j += 2) {
-        const int i = (c * V + j) / 2;
-        if (i < p.P) {
-          const float2 t = cs[i];
-          const float a = rope_f(v.e[j]), b = rope_f(v.e[j + 1]);
-          rope_put(v.e[j], fmaf(a, t.x, -b * t.y));
-          rope_put(v.e[j + 1], fmaf(b, t.x, a * t.y));
-        }
-      }
-      *reinterpret_cast<Vec*>(yh + c * V) = v;
-    } else if (c < turned) {
-      Vec v = *reinterpret_cast<const Vec*>(xh + c * V), w = *reinterpret_cast<const Vec*>(xh + p.P + c * V);
+  for (int j = 0; j < V; ++j) v.e[j] = f[j];
+}
+template <int V>
+__device__ __forceinline__ void rope_pack(const float (&f)[V], RopeVec<__nv_bfloat16, V>& v) {
+  if constexpr (V == 1) {
+    v.e[0] = __float2bfloat16_rn(f[0]);
+  } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 t = cs[c * V + j];
-        const float a = rope_f(v.e[j]), b = rope_f(w.e[j]);
-        rope_put(v.e[j], fmaf(a, t.x, -b * t.y));
-        rope_put(w.e[j], fmaf(b, t.x, a * t.y));
-      }
-      *reinterpret_cast<Vec*>(yh + c * V) = v;
-      *reinterpret_cast<Vec*>(yh + p.P + c * V) = w;
-    } else {
-      const int at = R + (c - turned) * V;
-      *reinterpret_cast<Vec*>(yh + at) = *reinterpret_cast<const Vec*>(xh + at);
+    for (int j = 0; j < V; j += 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[j], f[j + 1]);
+      reinterpret_cast<uint32_t*>(&v)[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
     }
   }
 }
 
-// cos, sin as [M, P] (row-major) or [P, M] (angle-major): one angle per thread and step,
-// neighbours in memory to neighbouring threads.
-template <bool kAngleMajor>
-__global__ void __launch_bounds__(256) rope_table_kernel(const RopeParams p) {
+// Pairs (a, b) turned, two at a time: (a c - b s, b c + a s).
+template <int N>
+__device__ __forceinline__ void rope_turn_pairs(float (&a)[N], float (&b)[N], const float (&c)[N], const float (&s)[N]) {
+#pragma unroll
+  for (int q = 0; q < N; q += 2) {
+    if constexpr (N % 2 == 0) {
+      const float2 av = make_float2(a[q], a[q + 1]), bv = make_float2(b[q], b[q + 1]);
+      const float2 cv = make_float2(c[q], c[q + 1]), sv = make_float2(s[q], s[q + 1]);
+      const float2 ra = __ffma2_rn(av, cv, __fmul2_rn(bv, make_float2(-sv.x, -sv.y)));
+      const float2 rb = __ffma2_rn(bv, cv, __fmul2_rn(av, sv));
+      a[q] = ra.x; a[q + 1] = ra.y;
+      b[q] = rb.x; b[q + 1] = rb.y;
+    } else {
+      const float av = a[q], bv = b[q];
+      a[q] = fmaf(av, c[q], -bv * s[q]);
+      b[q] = fmaf(bv, c[q], av * s[q]);
+    }
+  }
+}
+
+// A pair's fraction, axis and scale. An axis that the positions do not have: scale NaN, and
+// axis 0 read.
+struct RopePair {
+  uint64_t fraction;
+  int axis;
+  float scale;
+};
+__device__ __forceinline__ RopePair rope_pair(const RopeParams& p, int i) {
+  const int a = p.axis != nullptr ? p.axis[i] : 0;
+  const bool there = a >= 0 && a < p.A;
+  return {rope_fraction(p.freq[i]), there ? a : 0, there ? p.scale : __int_as_float(0x7fffffff)};
+}
+
+// One block per (row, share of the heads). The row's angles go through shared memory once;
+// then a thread keeps its V columns of a head (half layout: V of the first half and the V
+// they pair with), their cosines and sines in registers, and walks over the heads, with the
+// loads of kRopeHeads heads in flight, the first before the angles are made. Bound by HBM
+// (4608 rows of 60 heads of 128, bf16, 141.6 MB: RATE).
+constexpr int kRopeHeads = 4;
+template <typename T, int V, bool kInterleaved>
+__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+  __shared__ __align__(16) float cos_s[kRopeMaxPairs], sin_s[kRopeMaxPairs];
+  const size_t m = blockIdx.x;
+  const T* x = static_cast<const T*>(p.X) + m * p.ldx;
+  T* y = static_cast<T*>(p.Y) + m * p.ldy;
+  using Vec = RopeVec<T, V>;
+  // a head's units: interleaved, its V-element vectors; half layout, first those that hold
+  // pairs, then the copied ones
+  const int turned = p.P / V;
+  const int units = kInterleaved ? p.D / V : turned + (p.D - 2 * p.P) / V;
+  const int per_head = min(units, 256), heads_at_once = 256 / per_head;
+  const int group = threadIdx.x / per_head, step = heads_at_once * gridDim.y;
+  const int h0 = group < heads_at_once ? static_cast<int>(blockIdx.y) * heads_at_once + group : p.heads;
+  Vec v[kRopeHeads], w[kInterleaved ? 1 : kRopeHeads];
+  auto column = [&](int c) { return kInterleaved || c < turned ? c * V : 2 * p.P + (c - turned) * V; };
+  auto load = [&](int c, int h) {
+    const T* at = x + static_cast<size_t>(h) * p.ldhx + column(c);
+    const size_t next = static_cast<size_t>(step) * p.ldhx;
+#pragma unroll
+    for (int j = 0; j < kRopeHeads; ++j) {
+      if (h + j * step < p.heads) {
+        v[j] = *reinterpret_cast<const Vec*>(at);
+        if constexpr (!kInterleaved) {
+          if (c < turned) w[j] = *reinterpret_cast<const Vec*>(at + p.P);
+        }
+      }
+      at += next;
+    }
+  };
+  int c = threadIdx.x % per_head;
   grid_dep_wait();
   grid_dep_launch();
-  const size_t n = static_cast<size_t>(p.M) * p.P;
-  for (size_t k = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; k < n;
-       k += static_cast<size_t>(gridDim.x) * blockDim.x) {
-    const size_t m = kAngleMajor ? k % p.M : k / p.P;
-    const int i = static_cast<int>(kAngleMajor ? k / p.M : k % p.P);
-    const int a = p.axis != nullptr ? p.axis[i] : 0;
-    const float2 t = a >= 0 && a < p.A ? rope_cos_sin(rope_position(p, m, a), rope_fraction(p.freq[i]), p.scale)
-                                       : make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
-    p.cos[k] = t.x;
-    p.sin[k] = t.y;
+  load(c, h0);
+  for (int i = 2 * threadIdx.x; i < p.P; i += 2 * blockDim.x) {
+    const RopePair a = rope_pair(p, i), b = i + 1 < p.P ? rope_pair(p, i + 1) : a;
+    float2 cc, ss;
+    rope_cos_sin2(rope_turn(rope_position(p, m, a.axis), a.fraction), rope_turn(rope_position(p, m, b.axis), b.fraction),
+                  make_float2(a.scale, b.scale), cc, ss);
+    // (an odd last pair's neighbour is inside the arrays, and not read)
+    *reinterpret_cast<float2*>(cos_s + i) = cc;
+    *reinterpret_cast<float2*>(sin_s + i) = ss;
+  }
+  __syncthreads();
+  for (; c < units; c += per_head) {
+    constexpr int kPairs = kInterleaved ? V / 2 : V;
+    const int pairs = min(kPairs, p.P - c * kPairs);  // an interleaved unit may reach past the last pair
+    float ct[kPairs], st[kPairs];
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q)
+      if (q < pairs) {
+        ct[q] = cos_s[c * kPairs + q];
+        st[q] = sin_s[c * kPairs + q];
+      }
+    for (int h = h0; h < p.heads;) {
+      T* at = y + static_cast<size_t>(h) * p.ldhy + column(c);
+      const size_t next = static_cast<size_t>(step) * p.ldhy;
+#pragma unroll
+      for (int j = 0; j < kRopeHeads; ++j) {
+        if (h + j * step < p.heads) {
+          if constexpr (kInterleaved) {
+            if (pairs > 0) {
+              float f[V], a[kPairs], b[kPairs];
+              rope_unpack<V>(v[j], f);
+#pragma unroll
+              for (int q = 0; q < kPairs; ++q) a[q] = f[2 * q], b[q] = f[2 * q + 1];
+              rope_turn_pairs<kPairs>(a, b, ct, st);
+#pragma unroll
+              for (int q = 0; q < kPairs; ++q)
+                if (q < pairs) f[2 * q] = a[q], f[2 * q + 1] = b[q];
+              rope_pack<V>(f, v[j]);
+            }
+          } else if (pairs > 0 && c < turned) {
+            float a[V], b[V];
+            rope_unpack<V>(v[j], a);
+            rope_unpack<V>(w[j], b);
+            rope_turn_pairs<V>(a, b, ct, st);
+            rope_pack<V>(a, v[j]);
+            rope_pack<V>(b, w[j]);
+            *reinterpret_cast<Vec*>(at + p.P) = w[j];
+          }
+          *reinterpret_cast<Vec*>(at) = v[j];
+        }
+        at += next;
+      }
+      h += kRopeHeads * step;
+      if (h < p.heads) load(c, h);
+    }
+    if (c + per_head < units) load(c + per_head, h0);
+  }
+}
+
+// cos, sin as [M, P]: a thread keeps V adjacent pairs, their fractions in registers, and
+// walks down the rows, four at a time; pairs of one axis (most are) read its position once.
+// 131072 rows of 64 pairs, 67.6 MB: RATE.
+template <int V, typename Pos>
+__global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) {
+  const int nq = p.P / V, per_row = min(nq, 256), rows = 256 / per_row;
+  const int r = threadIdx.x / per_row;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (r >= rows) return;
+  const Pos* positions = static_cast<const Pos*>(p.positions);
+  for (int q = threadIdx.x % per_row; q < nq; q += per_row) {
+    RopePair pair[V];
+    bool one = true;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      pair[j] = rope_pair(p, q * V + j);
+      one = one && pair[j].axis == pair[0].axis;
+    }
+    const size_t step = static_cast<size_t>(gridDim.x) * rows;
+    auto put = [&](size_t m, const Pos (&pos)[V]) {
+      RopeVec<float, V> c, s;
+      if constexpr (V == 1) {
+        float2 cc, ss;
+        const uint32_t turn = rope_turn(pos[0], pair[0].fraction);
+        rope_cos_sin2(turn, turn, make_float2(pair[0].scale, pair[0].scale), cc, ss);
+        c.e[0] = cc.x;
+        s.e[0] = ss.x;
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+          float2 cc, ss;
+          rope_cos_sin2(rope_turn(pos[j], pair[j].fraction), rope_turn(pos[j + 1], pair[j + 1].fraction),
+                        make_float2(pair[j].scale, pair[j + 1].scale), cc, ss);
+          c.e[j] = cc.x, c.e[j + 1] = cc.y;
+          s.e[j] = ss.x, s.e[j + 1] = ss.y;
+        }
+      }
+      *reinterpret_cast<RopeVec<float, V>*>(p.cos + m * p.P + q * V) = c;
+      *reinterpret_cast<RopeVec<float, V>*>(p.sin + m * p.P + q * V) = s;
+    };
+    size_t m = static_cast<size_t>(blockIdx.x) * rows + r;
+    if (one) {
+      const Pos* at = positions + pair[0].axis;
+      for (; m < p.M; m += 4 * step) {
+        Pos four[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (m + k * step < p.M) four[k] = __ldg(at + (m + k * step) * p.A);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (m + k * step >= p.M) break;
+          Pos pos[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) pos[j] = four[k];
+          put(m + k * step, pos);
+        }
+      }
+    } else {
+      for (; m < p.M; m += step) {
+        Pos pos[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) pos[j] = __ldg(positions + m * p.A + pair[j].axis);
+        put(m, pos);
+      }
+    }
+  }
+}
+
+// cos, sin as [P, M]: neighbouring threads take neighbouring rows, a block up to
+// kRopeTablePairs pairs.
+constexpr int kRopeTablePairs = 8;
+__global__ void __launch_bounds__(256) rope_table_angle_major_kernel(const RopeParams p) {
+  const size_t m = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (m >= p.M) return;
+  const int end = min(p.P, static_cast<int>(blockIdx.y + 1) * kRopeTablePairs);
+#pragma unroll 4
+  for (int i = blockIdx.y * kRopeTablePairs; i < end; i += 2) {
+    const RopePair a = rope_pair(p, i), b = i + 1 < end ? rope_pair(p, i + 1) : a;
+    float2 c, s;
+    rope_cos_sin2(rope_turn(rope_position(p, m, a.axis), a.fraction), rope_turn(rope_position(p, m, b.axis), b.fraction),
+                  make_float2(a.scale, b.scale), c, s);
+    p.cos[static_cast<size_t>(i) * p.M + m] = c.x;
+    p.sin[static_cast<size_t>(i) * p.M + m] = s.x;
+    if (i + 1 < end) {
+      p.cos[static_cast<size_t>(i + 1) * p.M + m] = c.y;
+      p.sin[static_cast<size_t>(i + 1) * p.M + m] = s.y;
+    }
   }
 }
 

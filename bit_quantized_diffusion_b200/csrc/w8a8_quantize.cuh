@@ -7,7 +7,8 @@
 //
 // The norm's factor is one number per row, so max |y| = rsqrt(...) max |h weight|:
 // both reductions (the sum of squares, the maximum) run over the same registers and
-// meet in one block-wide exchange; the row is read once and kept in registers. The
+// meet in one block-wide exchange; the row is read once and kept in registers. Bound by
+// HBM. The
 // floor 2^-100 keeps 448 / t finite, so an all-zero row has scale 2^-100 / 448 and
 // codes 0 and no case of its own. The maximum is taken on the bits of |y|, where NaN
 // is above infinity is above every number: a row that holds NaN has scale NaN.
@@ -16,6 +17,9 @@
 #include "sm100.cuh"
 
 namespace svdq {
+
+// what a row goes through: codes alone, the norm first, the residual's addition before that
+enum W8Row : int { kW8Plain = 0, kW8Norm = 1, kW8ResidualNorm = 2 };
 
 struct W8QuantParams {
   int K;
@@ -26,7 +30,7 @@ struct W8QuantParams {
   void* residual_out;     // like X
   size_t ldo;
   const __nv_bfloat16* weight;  // [K] or null (1)
-  float eps;
+  float eps, inv_k;       // inv_k = 1 / K
   uint8_t* codes;         // [M, K]
   float* scale;           // [M]
 };
@@ -49,130 +53,266 @@ __device__ __forceinline__ W8Vec<kF32> w8_load(const void* base, size_t at) {
   return r;
 }
 template <bool kF32>
-__device__ __forceinline__ void w8_floats(const W8Vec<kF32>& r, float (&f)[8]) {
+__device__ __forceinline__ void w8_floats(const W8Vec<kF32>& r, float2 (&f)[4]) {
 #pragma unroll
   for (int i = 0; i < (kF32 ? 2 : 1); ++i) {
     const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+    if constexpr (kF32) {
+      f[2 * i] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      f[2 * i + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (kF32) {
-        f[4 * i + j] = __uint_as_float(w[j]);
-      } else {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
+      for (int j = 0; j < 4; ++j)
+        f[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
     }
   }
 }
 
+// max(|a|, |b|, |c|), NaN if one of them is
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // eight float32 -> eight E4M3 codes, element i in byte i
-__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8]) {
+__device__ __forceinline__ uint2 e4m3x8(const float2 (&v)[4]) {
   uint16_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+  for (int i = 0; i < 4; ++i) asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(v[i].y), "f"(v[i].x));
   return make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16));
 }
 
+// One vector of the row on its way into registers: the residual's sum and its copy out,
+// the weight (as float32, or null: from memory), and this thread's part of both reductions.
+template <int kRow, bool kF32>
+__device__ __forceinline__ void w8_take(const W8QuantParams& p, size_t row, int v, const W8Vec<kF32>& xv,
+                                        const W8Vec<kF32>& rv, const float2* wv, float2 (&h)[4], float2& ss,
+                                        float& top) {
+  w8_floats<kF32>(xv, h);
+  if (kRow != kW8Plain) {
+    if (kRow == kW8ResidualNorm) {
+      float2 r[4];
+      w8_floats<kF32>(rv, r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = __fadd2_rn(h[j], r[j]);
+      const size_t at = row * p.ldo + static_cast<size_t>(v) * 8;
+      if constexpr (kF32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.residual_out) + at);
+        o[0] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+        o[1] = make_float4(h[2].x, h[2].y, h[3].x, h[3].y);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 b = __float22bfloat162_rn(h[j]);
+          w[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual_out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ss = __ffma2_rn(h[j], h[j], ss);
+    if (p.weight != nullptr) {
+      float2 g[4];
+      if (wv != nullptr) {
+        const float4 a = reinterpret_cast<const float4*>(wv)[0], b = reinterpret_cast<const float4*>(wv)[1];
+        g[0] = make_float2(a.x, a.y), g[1] = make_float2(a.z, a.w);
+        g[2] = make_float2(b.x, b.y), g[3] = make_float2(b.z, b.w);
+      } else {
+        w8_floats<false>(w8_load<false>(p.weight, static_cast<size_t>(v) * 8), g);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = __fmul2_rn(h[j], g[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) top = max3_abs_nan(top, h[j].x, h[j].y);
+}
+
+// Both reductions over the block, through `part` [32] (zeros behind the last warp's), the
+// partial sums in an order of their own; false in every thread if `ok` is false in one.
+template <bool kNorm>
+__device__ __forceinline__ bool w8_reduce(float2 ss2, float top1, float& ss, float& top, bool ok, float2* part) {
+  const int warps = blockDim.x / 32;
+  // no sign: the bits are ordered like the numbers, NaN above them
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top1)));
+  ss = ss2.x + ss2.y;
+  if (kNorm) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  }
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_float2(ss, top);
+  ok = __syncthreads_and(ok);
+  if (warps <= 8) {
+    ss = top = 0.0f;
+    for (int i = 0; i < warps; i += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(part + i);
+      ss = ss + v.x + v.z;
+      top = max3_abs_nan(top, v.y, v.w);
+    }
+  } else {
+    const float2 v = part[threadIdx.x % 32];
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v.y)));
+    ss = v.x;
+    if (kNorm) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
+  }
+  return ok;
+}
+
+// The row's scale, and what turns its values into codes: one factor, or, where that would
+// leave float32's range (an all but empty row), rs and then inv.
+struct W8Factors {
+  float one, rs, inv;
+};
+template <bool kNorm>
+__device__ __forceinline__ W8Factors w8_scale(const W8QuantParams& p, size_t row, float ss, float top) {
+  W8Factors f;
+  float t = top;
+  f.rs = 1.0f;
+  if (kNorm) {
+    f.rs = rsqrtf(fmaf(ss, p.inv_k, p.eps));
+    t *= f.rs;
+  }
+  if (t < 7.888609052210118e-31f) t = 7.888609052210118e-31f;  // 2^-100; NaN stays
+  f.inv = __fdiv_rn(448.0f, t);
+  f.one = f.rs * f.inv;
+  if (threadIdx.x == 0) p.scale[row] = __fdiv_rn(t, 448.0f);
+  return f;
+}
+
+template <bool kNorm, int kVecs>
+__device__ __forceinline__ void w8_give(const W8QuantParams& p, size_t row, float2 (&h)[kVecs][4], const W8Factors& f) {
+  float mul = f.one;
+  if (kNorm && !(f.one < 1e37f)) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[i][j] = __fmul2_rn(h[i][j], make_float2(f.rs, f.rs));
+    mul = f.inv;
+  }
+  uint2* out = reinterpret_cast<uint2*>(p.codes + row * static_cast<size_t>(p.K)) + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+    if (static_cast<int>(threadIdx.x + i * blockDim.x) < p.K / 8) {
+      float2 q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = __fmul2_rn(h[i][j], make_float2(mul, mul));
+      out[i * blockDim.x] = e4m3x8(q);
+    }
+}
+
 // One block per row; thread i holds the row's 8-value vectors i, i + blockDim.x, ...
-template <bool kNorm, bool kF32, int kVecs>
+// For few rows, and for rows too long for the ring below.
+template <int kRow, bool kF32>
 __global__ void __launch_bounds__(1024) w8a8_quantize_kernel(const W8QuantParams p) {
+  constexpr bool kNorm = kRow != kW8Plain;
+  constexpr int kVecs = 4;
+  __shared__ __align__(16) float2 part[32];
   const size_t row = blockIdx.x;
   const int nvec = p.K / 8, T = blockDim.x, tid = threadIdx.x;
+  if (tid < 32 && tid >= T / 32) part[tid] = make_float2(0.0f, 0.0f);
   grid_dep_wait();
   grid_dep_launch();
-  float h[kVecs][8];
-  float ss = 0.0f;
-  uint32_t top = 0;
+  float2 h[kVecs][4], ss2 = make_float2(0.0f, 0.0f);
+  float ss, top = 0.0f;
   W8Vec<kF32> xv[kVecs], rv[kVecs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int v = tid + i * T;
     if (v < nvec) {
       xv[i] = w8_load<kF32>(p.X, row * p.ldx + static_cast<size_t>(v) * 8);
-      if (kNorm && p.residual != nullptr) rv[i] = w8_load<kF32>(p.residual, row * p.ldr + static_cast<size_t>(v) * 8);
+      if (kRow == kW8ResidualNorm) rv[i] = w8_load<kF32>(p.residual, row * p.ldr + static_cast<size_t>(v) * 8);
     }
   }
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int v = tid + i * T;
-    if (v < nvec) {
-      w8_floats<kF32>(xv[i], h[i]);
-      if (kNorm) {
-        if (p.residual != nullptr) {
-          float r[8];
-          w8_floats<kF32>(rv[i], r);
+  for (int i = 0; i < kVecs; ++i)
+    if (tid + i * T < nvec) w8_take<kRow, kF32>(p, row, tid + i * T, xv[i], rv[i], nullptr, h[i], ss2, top);
+  w8_reduce<kNorm>(ss2, top, ss, top, true, part);
+  const W8Factors f = w8_scale<kNorm>(p, row, ss, top);
+  w8_give<kNorm, kVecs>(p, row, h, f);
+}
+
+// Many rows: persistent blocks, each with a ring of rows (X, then the residual) that bulk
+// copies fill ahead, so that the loads go on through the reduction and the
+// stores of the row before.
+constexpr size_t kW8RingBytes = 227 * 1024;  // of an SM, for all its blocks' rings and weights
+constexpr size_t kW8RingOwn = 2048;          // a block's barriers and exchange, and what the system keeps
+constexpr int kW8RingStages = 2;
+struct W8RingParams {
+  int M;
+  uint32_t* status;
+};
+template <int kRow, bool kF32>
+__global__ void __launch_bounds__(1024) w8a8_quantize_ring_kernel(const W8QuantParams p,
+                                                                  const W8RingParams q) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) float2 part[2][32];
+  __shared__ uint64_t s_bars[kW8RingStages];
+  constexpr bool kNorm = kRow != kW8Plain, has_r = kRow == kW8ResidualNorm;
+  constexpr int kVecs = 4;
+  const int nvec = p.K / 8, T = blockDim.x, tid = threadIdx.x;
+  constexpr int NS = kW8RingStages;
+  const uint32_t x_bytes = p.K * (kF32 ? 4 : 2);
+  const uint32_t stage_bytes = has_r ? 2 * x_bytes : x_bytes;
+  const uint32_t bars = smem_u32(s_bars), base = smem_u32(ring);
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) mbar_init(bars + 8 * s, 1);
+    fence_barrier_init();
+  }
+  if (tid < 32 && tid >= T / 32) part[0][tid] = part[1][tid] = make_float2(0.0f, 0.0f);
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  auto fetch = [&](size_t row, int s) {
+    constexpr size_t esz = kF32 ? 4 : 2;
+    mbar_arrive_expect_tx(bars + 8 * s, stage_bytes);
+    bulk_load(base + s * stage_bytes, static_cast<const char*>(p.X) + row * p.ldx * esz, x_bytes, bars + 8 * s);
+    if (has_r)
+      bulk_load(base + s * stage_bytes + x_bytes, static_cast<const char*>(p.residual) + row * p.ldr * esz, x_bytes,
+                bars + 8 * s);
+  };
+  if (tid == 0)
+    for (int s = 0; s < NS; ++s)
+      if (blockIdx.x + static_cast<size_t>(s) * gridDim.x < q.M) fetch(blockIdx.x + static_cast<size_t>(s) * gridDim.x, s);
+  // the weight behind the ring, as float32: each thread reads back what it wrote itself
+  const bool has_w = kNorm && p.weight != nullptr;
+  float2* weight = reinterpret_cast<float2*>(ring + NS * stage_bytes);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-          const size_t at = row * p.ldo + static_cast<size_t>(v) * 8;
-          if constexpr (kF32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.residual_out) + at);
-            o[0] = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
-            o[1] = make_float4(h[i][4], h[i][5], h[i][6], h[i][7]);
-          } else {
-            uint32_t w[4];
+  for (int i = 0; i < kVecs; ++i)
+    if (has_w && tid + i * T < nvec) {
+      float2 g[4];
+      w8_floats<false>(w8_load<false>(p.weight, static_cast<size_t>(tid + i * T) * 8), g);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(h[i][2 * j], h[i][2 * j + 1]);
-              w[j] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual_out) + at) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+      for (int j = 0; j < 4; ++j) weight[(tid + i * T) * 4 + j] = g[j];
+    }
+  int s = 0, phase = 0, odd = 0;
+  for (size_t row = blockIdx.x; row < q.M; row += gridDim.x) {
+    bool ok = mbar_wait(bars + 8 * s, phase, q.status);
+    float2 h[kVecs][4], ss2 = make_float2(0.0f, 0.0f);
+    float ss, top = 0.0f;
+    const uint8_t* st = ring + s * stage_bytes;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
-        if (p.weight != nullptr) {
-          float g[8];
-          w8_floats<false>(w8_load<false>(p.weight, static_cast<size_t>(v) * 8), g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
-        }
+    for (int i = 0; i < kVecs; ++i) {
+      const int v = tid + i * T;
+      if (v < nvec) {
+        const W8Vec<kF32> xv = w8_load<kF32>(st, static_cast<size_t>(v) * 8);
+        W8Vec<kF32> rv = xv;
+        if (has_r) rv = w8_load<kF32>(st + x_bytes, static_cast<size_t>(v) * 8);
+        w8_take<kRow, kF32>(p, row, v, xv, rv, weight + v * 4, h[i], ss2, top);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(h[i][j]) & 0x7FFFFFFFu);
     }
-  }
-  // both reductions over the block
-  __shared__ float s_ss[32];
-  __shared__ uint32_t s_top[32];
-  const int warps = T / 32, warp = tid / 32, lane = tid % 32;
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (kNorm) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  }
-  if (warps > 1) {
-    if (lane == 0) {
-      s_top[warp] = top;
-      s_ss[warp] = ss;
-    }
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, lane < warps ? s_top[lane] : 0u);
-    if (kNorm) {
-      ss = lane < warps ? s_ss[lane] : 0.0f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    }
-  }
-  float t = __uint_as_float(top);
-  float rs = 1.0f;
-  if (kNorm) {
-    rs = 1.0f / sqrtf(ss / static_cast<float>(p.K) + p.eps);
-    t *= rs;
-  }
-  if (t < 7.888609052210118e-31f) t = 7.888609052210118e-31f;  // 2^-100; NaN stays
-  const float inv = 448.0f / t;
-  if (tid == 0) p.scale[row] = t / 448.0f;
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int v = tid + i * T;
-    if (v < nvec) {
-      float q[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = (kNorm ? h[i][j] * rs : h[i][j]) * inv;
-      *reinterpret_cast<uint2*>(p.codes + row * static_cast<size_t>(p.K) + static_cast<size_t>(v) * 8) = e4m3x8(q);
-    }
+    // the exchange's barrier also says that the stage has been read
+    if (!w8_reduce<kNorm>(ss2, top, ss, top, ok, part[odd])) break;
+    const size_t next = row + static_cast<size_t>(NS) * gridDim.x;
+    if (tid == 0 && next < q.M) fetch(next, s);
+    const W8Factors f = w8_scale<kNorm>(p, row, ss, top);
+    w8_give<kNorm, kVecs>(p, row, h, f);
+    odd ^= 1;
+    if (++s == NS) s = 0, phase ^= 1;
   }
 }
 

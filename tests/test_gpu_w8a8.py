@@ -50,7 +50,8 @@ def outer_is(whole, cols, fill):
 
 # ------------------------------------------------------------------ quantizer
 @TYPES
-@pytest.mark.parametrize("M,K", [(1, 16), (1, 3840), (3, 48), (7, 1040), (130, 512), (33, 4112), (2, 15360), (2, 32768)])
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 3840), (3, 48), (7, 1040), (130, 512), (33, 4112), (2, 15360), (2, 32768),
+                                 (9999, 64), (5001, 1040), (2300, 3856), (333, 16400)])
 def test_quantize_rows_bit_for_bit(bq, M, K, dtype):
     x = draw(M + K, M, K, dtype=dtype)
     x *= torch.logspace(-20, 20, M, device="cuda").to(dtype)[:, None] if M > 1 else 1
@@ -103,7 +104,8 @@ def check_norm(codes, scale, y, rel):
 @TYPES
 @pytest.mark.parametrize("M,K,weight,residual", [
     (1, 16, True, False), (1, 3840, True, True), (5, 48, False, True), (64, 1040, True, True), (3, 15360, True, True),
-    (2, 32768, False, False), (300, 512, True, True)])
+    (2, 32768, False, False), (300, 512, True, True), (9999, 64, True, True), (5001, 1040, True, False), (1501, 3840, True, True),
+    (333, 16400, False, True)])
 def test_rmsnorm_quantize(bq, M, K, weight, residual, dtype):
     x, w = draw(1, M, K, dtype=dtype), (1 + draw(2, K, std=0.2)).to(BF) if weight else None
     x[:, 3] *= 40
