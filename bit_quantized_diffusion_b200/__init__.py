@@ -386,86 +386,9 @@ def awq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, sz: torch.Tensor,
     return Y
 
 
-ACTIVATIONS = {None: N.ACT_NONE, "none": N.ACT_NONE, "gelu": N.ACT_GELU, "silu": N.ACT_SILU}
-_TYPES = {torch.bfloat16: N.OUT_BF16, torch.float32: N.OUT_F32}
-_E4M3 = torch.float8_e4m3fn
-_INT_MAX = 2 ** 31 - 1
-_POSITION_BYTES = {torch.int32: 4, torch.int64: 8}
-
-
-def _device() -> int | None:
-    """The current device's index; None where there is none (every tensor is refused then)."""
-    try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError):
-        return None
-
-
-def _refuse(t: torch.Tensor, shape: tuple, dtype, cur: int | None, name: str, how: str):
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.get_device() != cur:
-        raise ValueError(f"{name} on {t.device}, but the current device is cuda:{cur}: "
-                         f"call under torch.cuda.device({t.device})")
-    raise ValueError(f"{name}: {how}")
-
-
-# The checks of these calls run before every launch: one pass over what they need, the
-# reasons worked out only for a refusal.
-def _rows(t: torch.Tensor, shape: tuple, dtype, cur: int | None, name: str) -> tuple[int, int]:
-    """Address and row stride of a [rows, cols] tensor whose rows are contiguous."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == cur:
-        ld, one = t.stride()
-        if one == 1 and 0 <= ld <= _INT_MAX:
-            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
-    _refuse(t, shape, dtype, cur, name, "rows must be contiguous, their stride below 2^31")
-
-
-def _flat(t: torch.Tensor, shape: tuple, dtype, cur: int | None, name: str) -> int:
-    """Address of a contiguous tensor of one shape and type."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == cur and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, shape, dtype, cur, name, "must be contiguous")
-
-
-def _heads(t: torch.Tensor, shape: tuple, dtype, cur: int | None, name: str) -> tuple[int, int, int]:
-    """Address, row stride and head stride of a [M, heads, D] tensor with contiguous heads."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == cur:
-        ld, ldh, one = t.stride()
-        M, H, D = shape
-        ldh = ldh if H > 1 else D
-        ld = ld if M > 1 else H * ldh
-        if one == 1 and 0 <= ld <= _INT_MAX and 0 <= ldh <= _INT_MAX:
-            return t.data_ptr(), ld, ldh
-    _refuse(t, shape, dtype, cur, name, "heads must be contiguous, strides below 2^31")
-
-
-def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """Memory for an output, from the pool of the stream that the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _quantize_args(X, codes, scale, stream):
-    dtype, shape = X.dtype, X.shape
-    if len(shape) != 2 or dtype not in _TYPES:
-        raise ValueError("X must be a 2-D bf16 or float32 tensor")
-    M, K = shape
-    if M < 1 or K < 16 or K % 16 or K > 32768:
-        raise ValueError("X must be [M >= 1, K] with K a multiple of 16, at most 32768")
-    cur = _device()
-    x, ldx = _rows(X, shape, dtype, cur, "X")
-    if codes is None:
-        codes = _new(shape, _E4M3, X, stream)
-    if scale is None:
-        scale = _new((M,), torch.float32, X, stream)
-    return (shape, dtype, cur, x, ldx, codes, _flat(codes, shape, _E4M3, cur, "codes"), scale,
-            _flat(scale, (M,), torch.float32, cur, "scale"))
+# The 8-bit linear and rotary positions. Their checks and marshalling are compiled
+# (csrc/binding.cpp): these calls are short on the device and many in a decoding loop.
+# Given a ``stream``, what they allocate comes from that stream's pool.
 
 
 def w8a8_quantize_act(X: torch.Tensor, codes: torch.Tensor | None = None, scale: torch.Tensor | None = None,
@@ -473,10 +396,7 @@ def w8a8_quantize_act(X: torch.Tensor, codes: torch.Tensor | None = None, scale:
     """Rows of X [M, K] (bf16 or float32, row-strided) as E4M3 codes with a float32 scale
     each: X ~ codes * scale[:, None]. Weights [N, K] go through it too. Returns
     (codes float8_e4m3fn [M, K], scale float32 [M])."""
-    (M, K), dtype, cur, x, ldx, codes, pc, scale, ps = _quantize_args(X, codes, scale, stream)
-    N.check(N.load().w8a8_quantize_act(M, K, x, ldx, _TYPES[dtype], pc, ps, _stream(stream)),
-            "w8a8_quantize_act")
-    return codes, scale
+    return N.binding().w8a8_quantize_act(X, codes, scale, stream)
 
 
 def w8a8_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor | None = None,
@@ -487,54 +407,7 @@ def w8a8_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor | None = None,
     a float32 scale each. X and residual [M, K] bf16 or float32 (row-strided), weight bf16 [K]
     or None (1). Returns (codes, scale, residual_out): residual_out is h in X's type
     (residual or X itself may be passed for it: in place), None without a residual."""
-    shape, dtype, cur, x, ldx, codes, pc, scale, ps = _quantize_args(X, codes, scale, stream)
-    pr = po = None
-    ldr = ldo = 0
-    if residual is not None:
-        if residual_out is None:
-            residual_out = _new(shape, dtype, X, stream)
-        pr, ldr = _rows(residual, shape, dtype, cur, "residual")
-        po, ldo = _rows(residual_out, shape, dtype, cur, "residual_out")
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    M, K = shape
-    pw = None if weight is None else _flat(weight, (K,), torch.bfloat16, cur, "weight")
-    N.check(N.load().w8a8_rmsnorm_quantize(M, K, x, ldx, pr, ldr, pw, eps, po, ldo, _TYPES[dtype], pc, ps,
-                                           _stream(stream)), "w8a8_rmsnorm_quantize")
-    return codes, scale, residual_out
-
-
-def _w8a8(call: str, gated: bool, a_codes, a_scale, w_codes, w_scale, bias, residual, activation, out_dtype, Y,
-          stream):
-    shape_a, shape_w = a_codes.shape, w_codes.shape
-    if len(shape_a) != 2 or len(shape_w) != 2:
-        raise ValueError("a_codes and w_codes must be [M, K] and [N, K]")
-    M, K = shape_a
-    rows = shape_w[0]
-    cols = rows // 2 if gated else rows
-    if M < 1 or K < 16 or K % 16 or cols < 16 or cols % 16 or (gated and rows % 2) or shape_w[1] != K:
-        raise ValueError("a_codes [M, K] and w_codes must share K, at least one row, K and the output's width "
-                         "multiples of 16")
-    if out_dtype not in _TYPES:
-        raise ValueError("out_dtype must be bfloat16 or float32")
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}")
-    cur = _device()
-    if Y is None:
-        Y = _new((M, cols), out_dtype, a_codes, stream)
-    y, ldy = _rows(Y, (M, cols), out_dtype, cur, "Y")
-    args = (M, cols, K, _flat(a_codes, shape_a, _E4M3, cur, "a_codes"),
-            _flat(a_scale, (M,), torch.float32, cur, "a_scale"), _flat(w_codes, shape_w, _E4M3, cur, "w_codes"),
-            _flat(w_scale, (rows,), torch.float32, cur, "w_scale"),
-            None if bias is None else _flat(bias, (rows,), torch.bfloat16, cur, "bias"), ACTIVATIONS[activation])
-    lib = N.load()
-    if gated:
-        st = lib.w8a8_gated_linear(*args, y, ldy, _TYPES[out_dtype], _stream(stream))
-    else:
-        r, ldr = (None, 0) if residual is None else _rows(residual, (M, cols), out_dtype, cur, "residual")
-        st = lib.w8a8_linear(*args, r, ldr, y, ldy, _TYPES[out_dtype], _stream(stream))
-    N.check(st, call)
-    return Y
+    return N.binding().w8a8_rmsnorm_quantize(X, weight, residual, eps, codes, scale, residual_out, stream)
 
 
 def w8a8_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Tensor,
@@ -544,8 +417,8 @@ def w8a8_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: torch.Ten
     the rows of w8a8_quantize_act / w8a8_rmsnorm_quantize: a_codes [M, K], w_codes [N, K]
     float8_e4m3fn, bias bf16 [N], residual [M, N] of Y's type (Y itself may be passed: in
     place), activation None, "gelu" (tanh form) or "silu"."""
-    return _w8a8("w8a8_linear", False, a_codes, a_scale, w_codes, w_scale, bias, residual, activation, out_dtype, Y,
-                 stream)
+    return N.binding().w8a8_linear(a_codes, a_scale, w_codes, w_scale, bias, residual, activation, out_dtype, Y,
+                                   stream)
 
 
 def w8a8_gated_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Tensor,
@@ -553,23 +426,7 @@ def w8a8_gated_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: tor
                       Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [M, F] = act(gate) * up, where gate | up = a_codes w_codes^T * a_scale[:, None] *
     w_scale + bias, w_codes [2F, K] holding F gate rows and then F up rows."""
-    return _w8a8("w8a8_gated_linear", True, a_codes, a_scale, w_codes, w_scale, bias, None, activation, out_dtype, Y,
-                 stream)
-
-
-def _rope_args(positions, freq, axis, M, scale, cur):
-    """The arguments svdq_rope and svdq_rope_table share, in their order."""
-    dtype, shape, pairs = positions.dtype, positions.shape, freq.shape
-    if dtype not in _POSITION_BYTES or len(shape) not in (1, 2):
-        raise ValueError("positions must be int32 or int64, [M] or [M, axes]")
-    axes = shape[1] if len(shape) == 2 else 1
-    if shape[0] != M or axes < 1:
-        raise ValueError(f"positions must be [{M}] or [{M}, axes]")
-    if len(pairs) != 1:
-        raise ValueError("freq must be float64 [pairs]")
-    return (pairs[0], axes, _flat(positions, shape, dtype, cur, "positions"), _POSITION_BYTES[dtype],
-            _flat(freq, pairs, torch.float64, cur, "freq"),
-            None if axis is None else _flat(axis, pairs, torch.int32, cur, "axis"), scale)
+    return N.binding().w8a8_gated_linear(a_codes, a_scale, w_codes, w_scale, bias, activation, out_dtype, Y, stream)
 
 
 def svdq_rope(X: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, axis: torch.Tensor | None = None,
@@ -581,19 +438,7 @@ def svdq_rope(X: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, axis
     [pairs] (prep.rope_frequencies), 2 pairs <= D, the other columns copied; axis int32 [pairs]
     or None (0). Pairs are columns (2i, 2i + 1) if interleaved, else (i, i + pairs). ``scale``
     multiplies cosine and sine. Y may be X (in place)."""
-    shape, dtype = X.shape, X.dtype
-    if len(shape) != 3 or dtype not in _TYPES:
-        raise ValueError("X must be bf16 or float32 [M, heads, D]")
-    M, H, D = shape
-    cur = _device()
-    if Y is None:
-        Y = _new(shape, dtype, X, stream)
-    shared = _rope_args(positions, freq, axis, M, scale, cur)
-    if H < 1 or M < 1 or D % 2 or 2 * shared[0] > D:
-        raise ValueError("D must be even and hold 2 * len(freq) columns")
-    N.check(N.load().svdq_rope(M, H, D, *shared, bool(interleaved), _TYPES[dtype], *_heads(X, shape, dtype, cur, "X"),
-                               *_heads(Y, shape, dtype, cur, "Y"), _stream(stream)), "svdq_rope")
-    return Y
+    return N.binding().svdq_rope(X, positions, freq, axis, scale, interleaved, Y, stream)
 
 
 def svdq_rope_table(positions: torch.Tensor, freq: torch.Tensor, axis: torch.Tensor | None = None,
@@ -601,15 +446,7 @@ def svdq_rope_table(positions: torch.Tensor, freq: torch.Tensor, axis: torch.Ten
                     sin: torch.Tensor | None = None, stream=None):
     """(cos, sin) float32 [M, pairs] of svdq_rope's angles, or [pairs, M] with angle_major:
     the layout that svdq_w4a4_linear_qkv_norm_rope takes (64 pairs)."""
-    M = positions.shape[0] if positions.dim() else 0
-    cur = _device()
-    shared = _rope_args(positions, freq, axis, M, scale, cur)
-    shape = (shared[0], M) if angle_major else (M, shared[0])
-    cos = _new(shape, torch.float32, positions, stream) if cos is None else cos
-    sin = _new(shape, torch.float32, positions, stream) if sin is None else sin
-    pc, ps = _flat(cos, shape, torch.float32, cur, "cos"), _flat(sin, shape, torch.float32, cur, "sin")
-    N.check(N.load().svdq_rope_table(M, *shared, bool(angle_major), pc, ps, _stream(stream)), "svdq_rope_table")
-    return cos, sin
+    return N.binding().svdq_rope_table(positions, freq, axis, scale, angle_major, cos, sin, stream)
 
 
 def svdq_column_absmax(A: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:

@@ -7,6 +7,7 @@ implementation of these calls in this package.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -34,6 +35,22 @@ EXPORTS = (
 )
 
 _lib = None
+_binding = None
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
+
+
+def binding():
+    """The compiled binding (csrc/binding.cpp) of the 8-bit and rotary calls."""
+    global _binding
+    if _binding is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is missing: build it with `python -m bit_quantized_diffusion_b200.build`")
+        import torch  # noqa: F401  (its libraries are the binding's)
+        _binding = importlib.import_module(__package__ + "._binding")
+    return _binding
+
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int

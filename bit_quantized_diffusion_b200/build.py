@@ -1,4 +1,6 @@
-"""Build the sm_100a shared library ``libsvdq.so`` in-tree with nvcc.
+"""Build the sm_100a shared library ``libsvdq.so`` in-tree with nvcc, and the
+compiled binding ``_binding.so`` of the 8-bit and rotary calls above it with the
+host compiler.
 
     python -m bit_quantized_diffusion_b200.build
 
@@ -14,10 +16,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libsvdq.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_DEPS = [os.path.join(PKG, "csrc", "binding.cpp"), os.path.join(ROOT, "include", "svdq.h")]
 SOURCES = [os.path.join(PKG, "csrc", "svdq.cu")]
 DEPS = SOURCES + [os.path.join(PKG, "csrc", f) for f in os.listdir(os.path.join(PKG, "csrc"))
                   if f.endswith(".cuh")] + [os.path.join(ROOT, "include", "svdq.h")]
@@ -39,11 +44,28 @@ def command(out: str = LIB, verbose_ptxas: bool = False) -> list[str]:
     return cmd
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def binding_command(out: str = BINDING) -> list[str]:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler found")
+    # libsvdq.so is found beside the binding, so both bindings share one library
+    return [cxx, "-shared", "-fPIC", "-O2", "-std=c++17",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-o", out, BINDING_DEPS[0],
+            "-L", PKG, "-l:libsvdq.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(home, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def up_to_date(out: str = LIB, deps=DEPS) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in DEPS)
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(d) <= t for d in deps)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -51,6 +73,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         tmp = LIB + ".tmp"
         subprocess.run(command(tmp, verbose_ptxas), check=True)
         os.replace(tmp, LIB)
+    if force or not up_to_date(BINDING, BINDING_DEPS):
+        tmp = BINDING + ".tmp"
+        subprocess.run(binding_command(tmp), check=True)
+        os.replace(tmp, BINDING)
     return LIB
 
 

@@ -1197,10 +1197,15 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   p.residual = residual;
   p.ldr = ldr;
   p.status = d->status;
-  // Few tokens stream the weight (K = 3840, N = 15360 at 64 / 128 / 256 tokens: 16.5 / 20.1
-  // / 32.0 us against 20.3 / 21.7 / 23.3 in CTA pairs); above 64 only where K is long enough
-  // to hide the wider sum at its end (K = N = 1024 at 64 / 128: 5.0 / 6.6 against 5.2 / 5.2).
-  if (M <= 64 || (M <= kWsMaxT && K >= 2048)) return launch_w8a8_stream(d, gated, p, a_codes, w_codes, Y, ldy, stream);
+  // Few tokens stream the weight (64 tokens, streamed / in CTA pairs: K = N = 1024 5.0 / 4.8 us,
+  // K = N = 3840 8.8 / 10.1, K = 1024, N = 15360 9.9 / 12.1). Above 64 only where no CTA shares a
+  // tile's K, or K is long: the sum over a cluster grows with the tokens (128 tokens: K = N = 1024
+  // 6.5 / 5.2, K = 2048, N = 3840 9.1 / 8.4, K = N = 3840 10.8 / 10.6, K = 1024, N = 15360 12.7 / 12.9,
+  // K = 15360, N = 3840 18.2 / 26.4).
+  const int tile_rows = gated ? 64 : 128;
+  const bool unsplit = 5ll * ((N + tile_rows - 1) / tile_rows) >= 4ll * d->num_sms;
+  if (M <= 64 || (M <= kWsMaxT && (unsplit || K >= 3500)))
+    return launch_w8a8_stream(d, gated, p, a_codes, w_codes, Y, ldy, stream);
   // The tile's width: the one whose waves of tiles over the CTA pairs take least, a stage
   // of K costing its operands' way in, 256 + bn rows per pair (at 256 columns that equals its
   // MMA time). K = 3840: M = 256, N = 3840 takes 10.7 us at 64 columns and 18.4 at 256, M = 4608

@@ -583,12 +583,19 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   if (n < p.N) {
     for (; e < e1; e += kStep * kWsThreads) {
       float y[kStep][4];
+      float4 v4[kStep], w4[kStep];
+#pragma unroll
+      for (int j = 0; j < kStep; ++j)
+        if (e + j * kWsThreads < e1) {
+          v4[j] = sum4((e + j * kWsThreads) / kQuads, c);
+          if (kGated) w4[j] = sum4((e + j * kWsThreads) / kQuads, 64 + c);
+        }
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
         const int m = (e + j * kWsThreads) / kQuads;
         if (e + j * kWsThreads < e1) {
           const float sa = sa_s[m];
-          const float4 v = sum4(m, c);
+          const float4 v = v4[j];
           y[j][0] = fmaf(v.x * sa, sw[0], bias[0]);
           y[j][1] = fmaf(v.y * sa, sw[1], bias[1]);
           y[j][2] = fmaf(v.z * sa, sw[2], bias[2]);
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[j][q] = w8_act(y[j][q], p.act);
           if (kGated) {
-            const float4 w = sum4(m, 64 + c);
+            const float4 w = w4[j];
             y[j][0] *= fmaf(w.x * sa, sw[4], bias[4]);
             y[j][1] *= fmaf(w.y * sa, sw[5], bias[5]);
             y[j][2] *= fmaf(w.z * sa, sw[6], bias[6]);
