@@ -626,4 +626,108 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   if (kSplit) cluster_sync_converged();
 }
 
+// w8a8_gemv_kernel: up to 16 tokens of a small weight. There the tensor-memory kernels' set-up (tensor maps,
+// barriers, tensor memory, the first copy's way) is as long as reading the weight, so a
+// block of 16 weight rows (gated: 8 gate rows and the 8 matching up rows) reads it straight
+// into the fragments of the warp-level MMA, m16n8k32 on E4M3. The sum over k may run in any
+// order, so a lane's 16 bytes of a row are the fragments of two MMAs as they lie there, and
+// its 16 bytes of a token match them: neither operand passes through shared memory. Warps
+// take every other 64 bytes of K; their partial sums meet in shared memory in a fixed order.
+constexpr int kWvMaxM = 16;
+constexpr int kWvUnroll = 4;  // 64-byte steps whose loads are on their way together
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* at) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(at));
+  return v;
+}
+
+__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct WvParams {
+  int M, N, K;                 // N: output columns (F when gated)
+  const uint8_t* a;            // [M, K]
+  const uint8_t* w;            // [N, K] or, gated, [2 N, K]
+  int act, out_f32;
+  const float* a_scale;
+  const float* w_scale;
+  const __nv_bfloat16* bias;
+  const void* residual;
+  size_t ldr;
+  void* Y;
+  size_t ldy;
+};
+
+template <bool kGated, int kTokens8>  // kTokens8: groups of 8 tokens
+__global__ void __launch_bounds__(512) w8a8_gemv_kernel(const WvParams p) {
+  __shared__ float part[16][16 * 8 * kTokens8];  // [warp][weight row][token]
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane / 4, t = lane % 4;
+  constexpr int kCols = kGated ? 8 : 16;
+  const int n0 = blockIdx.x * kCols;
+  const size_t K = p.K;
+  const uint8_t* w0 = p.w + (static_cast<size_t>(n0) + g) * K + 16 * t;
+  const uint8_t* w1 = p.w + (static_cast<size_t>(kGated ? p.N + n0 : n0 + 8) + g) * K + 16 * t;
+  grid_dep_wait();
+  grid_dep_launch();
+  float acc[kTokens8][4] = {};
+  for (int k0 = 64 * warp; k0 < p.K; k0 += 64 * warps * kWvUnroll) {
+    uint4 a[kWvUnroll][2], b[kWvUnroll][kTokens8];
+#pragma unroll
+    for (int u = 0; u < kWvUnroll; ++u) {
+      const int k = k0 + 64 * warps * u;
+      const bool in = k + 16 * t < p.K;
+      a[u][0] = in ? ldg_stream(w0 + k) : make_uint4(0, 0, 0, 0);
+      a[u][1] = in ? ldg_stream(w1 + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < kTokens8; ++j)
+        b[u][j] = in && 8 * j + g < p.M
+                      ? __ldg(reinterpret_cast<const uint4*>(p.a + (8 * j + g) * K + k + 16 * t))
+                      : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kWvUnroll; ++u)
+#pragma unroll
+      for (int j = 0; j < kTokens8; ++j) {
+        mma_e4m3_16832(acc[j], a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u][j].x, b[u][j].y);
+        mma_e4m3_16832(acc[j], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][j].z, b[u][j].w);
+      }
+  }
+  // (row g, tokens 2t, 2t + 1) and (row g + 8, the same tokens) of each group of tokens
+#pragma unroll
+  for (int j = 0; j < kTokens8; ++j) {
+    part[warp][(8 * j + 2 * t) * 16 + g] = acc[j][0];
+    part[warp][(8 * j + 2 * t + 1) * 16 + g] = acc[j][1];
+    part[warp][(8 * j + 2 * t) * 16 + g + 8] = acc[j][2];
+    part[warp][(8 * j + 2 * t + 1) * 16 + g + 8] = acc[j][3];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.M * kCols; e += blockDim.x) {
+    const int m = e / kCols, c = e % kCols, n = n0 + c;
+    auto z = [&](int row16, int row) {
+      float s = part[0][m * 16 + row16];
+      for (int i = 1; i < warps; ++i) s += part[i][m * 16 + row16];
+      return fmaf(s * p.a_scale[m], p.w_scale[row], p.bias != nullptr ? __bfloat162float(p.bias[row]) : 0.0f);
+    };
+    float y = w8_act(z(c, n), p.act);
+    if (kGated) y *= z(c + 8, p.N + n);
+    const size_t at = static_cast<size_t>(m) * p.ldy + n, ar = static_cast<size_t>(m) * p.ldr + n;
+    if (p.out_f32) {
+      if (p.residual != nullptr) y += static_cast<const float*>(p.residual)[ar];
+      static_cast<float*>(p.Y)[at] = y;
+    } else {
+      if (p.residual != nullptr) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[ar]);
+      static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(y);
+    }
+  }
+}
+
 }  // namespace svdq
