@@ -1207,6 +1207,7 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   if (M < 1 || N < 16 || N % 16 || K < 16 || K % 16 || ldy < N || (gated && N > INT32_MAX / 2))
     return SVDQ_ERR_INVALID_ARG;
   if (!a_codes || !a_scale || !w_codes || !w_scale || !Y || (residual && ldr < N)) return SVDQ_ERR_INVALID_ARG;
+  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return SVDQ_ERR_UNSUPPORTED;  // tile corners stay in an int
   const size_t esz = out == SVDQ_OUT_F32 ? 4 : 2;
   if (!aligned16(a_codes) || !aligned16(w_codes) || !aligned16(Y) || (ldy * esz) % 16 || !aligned4(a_scale) ||
       !aligned4(w_scale) || (bias && (reinterpret_cast<uintptr_t>(bias) & 1u)) ||

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     if (elect_one()) {
       bool ok = true;
       int s = 0, phase = 0;  // ring stage, and the parity of its use
+      long long loads = 0;
       for (int i = 0; i < my_tiles && ok; ++i) {
         int m0, n0;
         tile_mn(i, m0, n0);
@@ -164,7 +165,14 @@ __global__ void __launch_bounds__(kW8Threads, 1)
           tma_load_2d_pair(a_st(s), &tm_a, fb, kt * kW8KStage, mrow);
           tma_load_2d_pair(b_st(s), &tm_b, fb, kt * kW8KStage, nrow);
           if (++s == NS) s = 0, phase ^= 1;
+          ++loads;
         }
+      }
+      // No CTA of the pair leaves (they meet at the end) before the last loads have landed, also
+      // after a wait has run out
+      for (int back = 1; leader && back <= NS && back <= loads; ++back) {
+        if (--s < 0) s = NS - 1, phase ^= 1;
+        mbar_wait(bar_full(s), phase, p.status);
       }
     }
   } else if (warp == 1) {
@@ -520,11 +528,15 @@ __global__ void __launch_bounds__(kWsThreads, 2)
 
   if (warp == 0) {
     if (lane == 0) {
+      int last = min(NS, k1 - k0) - 1;
       for (int g = NS; k0 + g < k1; ++g) {
         const int s = g % NS;
         if (!mbar_wait(bar_empty(s), ((g / NS) & 1) ^ 1, p.status)) break;
         load(k0 + g, s);
+        last = g;
       }
+      // the last loads have landed before the block ends, also after a wait has run out
+      for (int g = max(0, last - NS + 1); g <= last; ++g) mbar_wait(bar_full(g % NS), (g / NS) & 1, p.status);
     }
   } else if (warp == 1) {
     if (elect_one()) {

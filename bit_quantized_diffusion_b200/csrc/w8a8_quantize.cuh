@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(1024) w8a8_quantize_ring_kernel(const W8QuantP
   constexpr int kVecs = 4;
   const int nvec = p.K / 8, T = blockDim.x, tid = threadIdx.x;
   constexpr int NS = kW8RingStages;
+  static_assert(NS == 2, "the other stage is s ^ 1");
   const uint32_t x_bytes = p.K * (kF32 ? 4 : 2);
   const uint32_t stage_bytes = has_r ? 2 * x_bytes : x_bytes;
   const uint32_t bars = smem_u32(s_bars), base = smem_u32(ring);
@@ -306,7 +307,14 @@ __global__ void __launch_bounds__(1024) w8a8_quantize_ring_kernel(const W8QuantP
       }
     }
     // the exchange's barrier also says that the stage has been read
-    if (!w8_reduce<kNorm>(ss2, top, ss, top, ok, part[odd])) break;
+    if (!w8_reduce<kNorm>(ss2, top, ss, top, ok, part[odd])) {
+      // a wait has run out: the copies on their way land (or run out again) before the block ends
+      if (tid == 0) {
+        mbar_wait(bars + 8 * s, phase, q.status);
+        if (row + gridDim.x < q.M) mbar_wait(bars + 8 * (s ^ 1), s == 0 ? phase : phase ^ 1, q.status);
+      }
+      break;
+    }
     const size_t next = row + static_cast<size_t>(NS) * gridDim.x;
     if (tid == 0 && next < q.M) fetch(next, s);
     const W8Factors f = w8_scale<kNorm>(p, row, ss, top);

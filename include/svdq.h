@@ -491,7 +491,8 @@ svdq_status awq_quantize_weight(int N, int K, const void* W, void* qweight, void
  *   z as above (without residual) for n < 2F,  Y[m,n] = act(z[m,n]) * z[m,F+n]
  *   w_codes [2F, K], w_scale [2F], bias bf16 [2F] or NULL, Y [M, ldy >= F];  F % 16 == 0
  *
- * INVALID_ARG / ALIGNMENT on bad arguments, before any launch.
+ * INVALID_ARG / ALIGNMENT on bad arguments, UNSUPPORTED where M, N or K of a product
+ * passes 2^30, before any launch.
  */
 svdq_status w8a8_quantize_act(int M, int K, const void* X, int ldx, svdq_out dtype, void* codes, float* scale,
                               svdq_stream_t stream);
@@ -529,7 +530,8 @@ svdq_status w8a8_gated_linear(int M, int F, int K, const void* a_codes, const fl
  * svdq_rope_table -- the tables alone: cos, sin float32 [M, pairs], or [pairs, M] with
  * angle_major (the layout svdq_w4a4_linear_qkv_norm_rope takes, with pairs = 64).
  *
- * INVALID_ARG / ALIGNMENT on bad arguments, before any launch.
+ * INVALID_ARG / ALIGNMENT on bad arguments, UNSUPPORTED where heads * head_dim passes
+ * 2^30, before any launch.
  */
 svdq_status svdq_rope(int M, int heads, int head_dim, int pairs, int axes, const void* positions, int position_bytes,
                       const double* freq, const int* axis, float scale, int interleaved, svdq_out dtype,

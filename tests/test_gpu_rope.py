@@ -195,3 +195,20 @@ def test_layer_rotates_and_feeds_the_fused_projection(bq):
     graph.replay()
     assert torch.equal(y, rot(plain[:, : 2 * H], pos)) and not torch.equal(y, again)
     assert bq.svdq_check_device_status() == 0
+
+
+def test_offsets_beyond_32_bits(bq):
+    """Heads whose elements number over 2^32, in place: the last rows agree with a call on them alone."""
+    M, H, D = 70_000, 64, 1024
+    x = torch.empty(M, H, D, dtype=BF, device="cuda")
+    x[-2:] = torch.randn(2, H, D, generator=torch.Generator().manual_seed(0)).to(BF).cuda()
+    pos = torch.arange(M, dtype=torch.int64, device="cuda")
+    freq = torch.logspace(0, -3, 512, dtype=torch.float64).cuda()
+    want = bq.svdq_rope(x[-2:], pos[-2:], freq)
+    bq.svdq_rope(x, pos, freq, Y=x)
+    assert torch.equal(x[-2:], want)
+    del x
+    M, P = 8_400_000, 512
+    cos, sin = bq.svdq_rope_table(torch.arange(M, dtype=torch.int32, device="cuda"), freq)
+    c, s = bq.svdq_rope_table(torch.arange(M - 3, M, dtype=torch.int32, device="cuda"), freq)
+    assert torch.equal(cos[-3:], c) and torch.equal(sin[-3:], s)

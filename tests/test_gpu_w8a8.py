@@ -345,6 +345,70 @@ def test_gated_block_together(bq, M):
     assert bq.svdq_check_device_status() == 0
 
 
+def test_offsets_beyond_32_bits(bq):
+    """Rows, outputs and residuals whose elements number over 2^32: the last rows and one in the
+    middle agree with calls on those rows alone."""
+    def rows_of(M):
+        return [0, M // 2 + 1, M - 2, M - 1]
+
+    M, K = 262_300, 16_384
+    x = torch.empty(M, K, dtype=BF, device="cuda")
+    pattern = draw(1, 4, K, dtype=BF)
+    for i, row in enumerate(rows_of(M)):
+        x[row] = pattern[i]
+    codes, scale = bq.w8a8_quantize_act(x)
+    want, want_scale = bq.w8a8_quantize_act(pattern)
+    assert torch.equal(codes[rows_of(M)].view(torch.uint8), want.view(torch.uint8))
+    assert torch.equal(scale[rows_of(M)], want_scale)
+    del x, codes
+    M, N, K = 1_050_000, 4112, 32
+    w, sw = bq.w8a8_quantize_act(draw(2, N, K))
+    a = torch.zeros(M, K, device="cuda").to(E4)
+    few = draw(3, 4, K).to(E4)
+    y = torch.zeros(M, N, dtype=BF, device="cuda")
+    r = draw(4, 4, N, dtype=BF)
+    for i, row in enumerate(rows_of(M)):
+        a.view(torch.uint8)[row] = few.view(torch.uint8)[i]
+        y[row] = r[i]
+    sa = torch.ones(M, device="cuda")
+    bq.w8a8_linear(a, sa, w, sw, residual=y, Y=y)
+    want = bq.w8a8_linear(few, sa[:4], w, sw, residual=r)
+    # one sum of 32 products, in one matrix instruction or another: the same to bf16's half step
+    assert torch.allclose(y[rows_of(M)].float(), want.float(), rtol=2.0 ** -8 + 2.0 ** -20, atol=1e-5)
+    assert bq.svdq_check_device_status() == 0
+
+
+def test_threads_and_stream_handles(bq):
+    """Calls from several threads on streams of their own, outputs allocated by the calls, the
+    stream given as an object or as its handle."""
+    import threading
+    K, N = 1040, 272
+    w, sw = bq.w8a8_quantize_act(draw(1, N, K, std=0.02))
+    x = [draw(10 + i, 30 + 50 * i, K, dtype=BF) for i in range(4)]
+    want = [bq.w8a8_linear(*bq.w8a8_quantize_act(t), w, sw) for t in x]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def run(i):
+        try:
+            s = torch.cuda.Stream()
+            handle = s if i % 2 else s.cuda_stream
+            for _ in range(20):
+                codes, scale = bq.w8a8_quantize_act(x[i], stream=handle)
+                y = bq.w8a8_linear(codes, scale, w, sw, stream=handle)
+            s.synchronize()
+            got[i] = y
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_other_device_is_refused(bq):
     if torch.cuda.device_count() < 2:
         x = torch.zeros(4, 64, dtype=BF)

@@ -69,6 +69,7 @@ def test_linear_argument_errors(lib):
 
     assert d(F=24) == ARG and d(act=5) == ARG and d(ldy=31) == ARG and d(Y=None) == ARG
     assert d(F=2 ** 30, ldy=2 ** 30) == ARG and d(Y=ODD8) == ALIGN
+    assert g(M=2 ** 30 + 1) == 3 and g(K=2 ** 30 + 16) == 3 and g(N=2 ** 30 + 16, ldy=2 ** 30 + 16) == 3
 
 
 def test_rope_argument_errors(lib):
@@ -83,6 +84,7 @@ def test_rope_argument_errors(lib):
     assert r(nb=2) == ARG and r(scale=math.nan) == ARG and r(scale=math.inf) == ARG and r(dtype=2) == ARG
     assert r(ldx=127) == ARG and r(ldhy=65, ldy=200) == ARG and r(ldx=-128) == ARG
     assert r(ldy=64) == ARG and r(ldhy=32) == ARG and r(ldy=126) == ARG   # rows or heads of Y meet
+    assert r(H=2 ** 20, D=2048, ldhx=2048, ldhy=2048, ldy=2 ** 31 - 2) == 3
     assert r(X=ODD8) == ALIGN and r(Y=ODD8) == ALIGN and r(pos=ODD2) == ALIGN and r(freq=P(0x10004)) == ALIGN
     assert r(pos=P(0x10004), nb=8) == ALIGN and r(axis=ODD2) == ALIGN
 
