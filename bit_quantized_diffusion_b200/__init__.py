@@ -406,7 +406,8 @@ def w8a8_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor | None = None,
     """h = X + residual; y = h / sqrt(mean(h^2) + eps) * weight; rows of y as E4M3 codes with
     a float32 scale each. X and residual [M, K] bf16 or float32 (row-strided), weight bf16 [K]
     or None (1). Returns (codes, scale, residual_out): residual_out is h in X's type
-    (residual or X itself may be passed for it: in place), None without a residual."""
+    (residual or X itself may be passed for it: in place), None without a residual. The norm
+    reads h before that rounding. K is a multiple of 16, at most 32768, here and above."""
     return N.binding().w8a8_rmsnorm_quantize(X, weight, residual, eps, codes, scale, residual_out, stream)
 
 
@@ -415,8 +416,8 @@ def w8a8_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: torch.Ten
                 out_dtype=torch.bfloat16, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [M, N] = act(a_codes w_codes^T * a_scale[:, None] * w_scale + bias) + residual, from
     the rows of w8a8_quantize_act / w8a8_rmsnorm_quantize: a_codes [M, K], w_codes [N, K]
-    float8_e4m3fn, bias bf16 [N], residual [M, N] of Y's type (Y itself may be passed: in
-    place), activation None, "gelu" (tanh form) or "silu"."""
+    float8_e4m3fn, K and N multiples of 16, bias bf16 [N], residual [M, N] of Y's type (Y
+    itself may be passed: in place), activation None, "gelu" (tanh form) or "silu"."""
     return N.binding().w8a8_linear(a_codes, a_scale, w_codes, w_scale, bias, residual, activation, out_dtype, Y,
                                    stream)
 
@@ -425,7 +426,8 @@ def w8a8_gated_linear(a_codes: torch.Tensor, a_scale: torch.Tensor, w_codes: tor
                       bias: torch.Tensor | None = None, activation="silu", out_dtype=torch.bfloat16,
                       Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [M, F] = act(gate) * up, where gate | up = a_codes w_codes^T * a_scale[:, None] *
-    w_scale + bias, w_codes [2F, K] holding F gate rows and then F up rows."""
+    w_scale + bias, w_codes [2F, K] holding F gate rows and then F up rows; K and F multiples
+    of 16. Gate and up stay in float32 up to their product."""
     return N.binding().w8a8_gated_linear(a_codes, a_scale, w_codes, w_scale, bias, activation, out_dtype, Y, stream)
 
 

@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   // The next grid's set-up under this one's work; but where this grid's blocks share SMs, only
   // at its end: the next one's blocks would take the second places (gated, 4 x 3840 x 10240, calls
   // in a row: 18.8 us, and 15.2 at the end).
-  if (!p.shared) grid_dep_launch();
   grid_dep_wait();
+  if (!p.shared) grid_dep_launch();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 

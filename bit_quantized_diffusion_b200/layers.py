@@ -234,7 +234,9 @@ class W8A8GatedMlp:
     """A pre-norm gated feed-forward block in 8 bits, on the residual stream:
     h = x (+ residual);  out = h + down(act(gate(norm(h))) * up(norm(h))), four calls:
     norm into E4M3, the gated product, its rows into E4M3, the second projection with h added in its
-    epilogue. ``up`` holds the F gate rows and then the F up rows [2F, K]; ``down`` [K, F]."""
+    epilogue. ``up`` holds the F gate rows and then the F up rows [2F, K]; ``down`` [K, F].
+    The hidden rows pass through bf16 on their way into E4M3 (their scale needs the whole
+    row, which no tile of the product holds): 2^-8 of a value beside E4M3's 2^-4."""
 
     def __init__(self, up: dict, down: dict, norm: torch.Tensor | None, max_tokens: int, activation: str = "silu",
                  eps: float = 1e-6):

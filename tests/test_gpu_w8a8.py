@@ -345,6 +345,37 @@ def test_gated_block_together(bq, M):
     assert bq.svdq_check_device_status() == 0
 
 
+@pytest.mark.parametrize("M", [1, 8, 40, 100, 300, 1500])
+def test_chain_on_one_buffer(bq, M):
+    """Layer after layer on one residual stream and one set of workspaces, each call reading what
+    the one before wrote over the values that the one before that had read: the bits of the same
+    chain with a new tensor for every result."""
+    from bit_quantized_diffusion_b200.layers import RotaryEmbedding, W8A8GatedMlp, W8A8Linear
+    K, F = 512, 656
+    blocks = [W8A8GatedMlp.from_linears(draw(i, F, K, dtype=BF, std=0.04), draw(i + 50, F, K, dtype=BF, std=0.04),
+                                        draw(i + 100, K, F, dtype=BF, std=0.03), None, max_tokens=M) for i in range(3)]
+    lin = W8A8Linear.from_linear(draw(7, K, K, dtype=BF, std=0.03), None, max_tokens=M)
+    rot = RotaryEmbedding(64)
+    pos = torch.arange(M, device="cuda")
+    x = draw(9, M, K, dtype=BF)
+
+    def chain(fresh):
+        h = x.clone()
+        for step in range(12):
+            y = None if fresh else h
+            h = blocks[step % 3](h, y=y)
+            y = None if fresh else h
+            h = rot(h.view(M, 8, 64), pos, y=None if fresh else y.view(M, 8, 64)).view(M, K)
+            y = None if fresh else h
+            h = lin(h, residual=h, y=y)
+        return h
+
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
+    assert torch.isfinite(want.float()).all() and bq.svdq_check_device_status() == 0
+
+
 def test_offsets_beyond_32_bits(bq):
     """Rows, outputs and residuals whose elements number over 2^32: the last rows and one in the
     middle agree with calls on those rows alone."""
