@@ -158,9 +158,13 @@ svdq_status device_setup(DeviceInfo** out) {
         cudaFuncSetAttribute(w4a4_mlp_fc1_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kMlSmemBytes)) != cudaSuccess ||
         w8a8_quantize_attributes() != cudaSuccess ||
-        cudaFuncSetAttribute(w8a8_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(w8a8_gemm_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kW8SmemBytes)) != cudaSuccess ||
-        cudaFuncSetAttribute(w8a8_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(w8a8_gemm_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kW8SmemBytes)) != cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_gemm_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kW8SmemBytes)) != cudaSuccess ||
+        cudaFuncSetAttribute(w8a8_gemm_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kW8SmemBytes)) != cudaSuccess ||
         cudaFuncSetAttribute(w8a8_stream_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) !=
             cudaSuccess ||
@@ -182,8 +186,10 @@ svdq_status device_setup(DeviceInfo** out) {
                           reinterpret_cast<const void*>(w4a4_int4_gemm_kernel<true>),
                           reinterpret_cast<const void*>(awq_gemm_kernel),
                           reinterpret_cast<const void*>(w4a4_mlp_fc1_kernel),
-                          reinterpret_cast<const void*>(w8a8_gemm_kernel<false>),
-                          reinterpret_cast<const void*>(w8a8_gemm_kernel<true>),
+                          reinterpret_cast<const void*>(w8a8_gemm_kernel<false, false>),
+                          reinterpret_cast<const void*>(w8a8_gemm_kernel<false, true>),
+                          reinterpret_cast<const void*>(w8a8_gemm_kernel<true, false>),
+                          reinterpret_cast<const void*>(w8a8_gemm_kernel<true, true>),
                           reinterpret_cast<const void*>(w8a8_stream_kernel<false, false>),
                           reinterpret_cast<const void*>(w8a8_stream_kernel<false, true>),
                           reinterpret_cast<const void*>(w8a8_stream_kernel<true, false>),
@@ -225,7 +231,7 @@ svdq_status device_setup(DeviceInfo** out) {
       d.gemm_pairs = pairs(w4a4_nvfp4_gemm_kernel<true>, kGmThreads, GmCfg<true>::kSmemBytes);
       d.int4_pairs = pairs(w4a4_int4_gemm_kernel<true>, kI4Threads, kI4SmemBytes);
       d.mlp_pairs = pairs(w4a4_mlp_fc1_kernel, kMlThreads, kMlSmemBytes);
-      d.w8_pairs = pairs(w8a8_gemm_kernel<false>, kW8Threads, kW8SmemBytes);
+      d.w8_pairs = pairs(w8a8_gemm_kernel<false, false>, kW8Threads, kW8SmemBytes);
       if (std::getenv("SVDQ_DEBUG") != nullptr)
         std::fprintf(stderr, "svdq: %d SMs, %d / %d co-resident NVFP4 / INT4 GEMM CTA pairs\n",
                      d.num_sms, d.gemm_pairs, d.int4_pairs);
@@ -1226,6 +1232,8 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   p.bias = static_cast<const __nv_bfloat16*>(bias);
   p.residual = residual;
   p.ldr = ldr;
+  p.Y = Y;
+  p.ldy = ldy;
   p.status = d->status;
   // One to sixteen tokens of a small weight: no set-up (one token: K = N = 1024 2.5 us against 3.7
   // streamed, K = N = 3840 5.9 against 7.1; sixteen: K = N = 1024 2.9 against 4.0). Where a warp would go
@@ -1272,20 +1280,18 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   p.band_tiles = p.band * (p.tiles / p.tiles_m);
   p.stages = static_cast<int>(kW8Ring / (kW8AStage + p.bn / 2 * kW8KStage));
   if (p.stages > kW8MaxStages) p.stages = kW8MaxStages;
-  CUtensorMap tm_a, tm_b, tm_y;
-  const bool f32 = out == SVDQ_OUT_F32;
+  CUtensorMap tm_a, tm_b;
   if (!make_tmap_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, K, M, K, kW8KStage, kW8BM,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, K, gated ? 2ull * N : N, K, kW8KStage,
-                    p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      // output: 32 x 32 boxes, bf16 rows of 64 B (64-byte swizzle) or f32 rows of 128 B
-      !make_tmap_2d(&tm_y, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M,
-                    ldy * esz, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+                    p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return SVDQ_ERR_CUDA;
   const int units = p.tiles < d->w8_pairs ? p.tiles : d->w8_pairs;
-  auto kern = gated ? w8a8_gemm_kernel<true> : w8a8_gemm_kernel<false>;
+  const bool f32 = out == SVDQ_OUT_F32;
+  auto kern = gated ? (f32 ? w8a8_gemm_kernel<true, true> : w8a8_gemm_kernel<true, false>)
+                    : (f32 ? w8a8_gemm_kernel<false, true> : w8a8_gemm_kernel<false, false>);
   if (launch_kernel(d, kern, dim3(units * 2), dim3(kW8Threads), kW8SmemBytes, static_cast<cudaStream_t>(stream), 2,
-                    tm_a, tm_b, tm_y, p) != cudaSuccess) {
+                    tm_a, tm_b, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return SVDQ_ERR_CUDA;
   }

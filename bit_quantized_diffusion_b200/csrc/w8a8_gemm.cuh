@@ -20,10 +20,13 @@
 // Warp roles per CTA (10 warps):
 //   warp 0     TMA producer
 //   warp 1     tensor-memory owner; in the leader CTA also the MMA issuer (one thread)
-//   warps 2-9  epilogue, two warps per tensor-memory lane quadrant
+//   warps 2-9  epilogue, two warps per tensor-memory lane quadrant: accumulator -> shared
+//              memory -> scales, bias, activation, residual -> memory
 // Tensor memory holds two accumulators of up to 256 columns, so a tile's epilogue runs under
 // the next tile's MMAs.
 #pragma once
+
+#include <type_traits>
 
 #include "sm100.cuh"
 
@@ -60,6 +63,8 @@ struct W8Params {
   const __nv_bfloat16* bias;   // like w_scale, or null
   const void* residual;        // the output's type, row stride ldr, or null
   int ldr;
+  void* Y;
+  int ldy;
   uint32_t* status;
 };
 
@@ -89,10 +94,26 @@ __device__ __forceinline__ float w8_act(float y, int act) {
   return __fdividef(y, 1.0f + __expf(e));
 }
 
-template <bool kGated>
+// Each thread reads 16 consecutive columns of its lane from either address.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t a, uint32_t b, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(b));
+}
+
+template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kW8Threads, 1)
     w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                     const __grid_constant__ CUtensorMap tm_y, const W8Params p) {
+                     const W8Params p) {
   const int NS = p.stages, half_n = p.bn / 2;
   const int tile_n = kGated ? half_n : p.bn;  // output columns per tile
   const uint32_t stage_bytes = kW8AStage + static_cast<uint32_t>(half_n) * kW8KStage;
@@ -134,7 +155,6 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     fence_barrier_init();
     prefetch_tmap(&tm_a);
     prefetch_tmap(&tm_b);
-    prefetch_tmap(&tm_y);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -208,28 +228,78 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     const int quad = warp & 3;         // tensor-memory lanes 32 quad .. 32 quad + 31
     const int half = (warp - 2) >> 2;  // which of the quadrant's two warps: it takes every other sub-tile
     const int ew = warp - 2;
-    const uint32_t out_buf = sbase + kW8Out + ew * kW8StageOut;
+    // A sub-tile (kCols output columns; gated, 16 gate and the 16 up columns) goes through shared
+    // memory as it is, one row per lane (float32, 128-byte rows, gated 64-byte rows of gate and
+    // of up, 16-byte units swizzled), and comes out in pieces of kWide adjacent columns, a row's
+    // pieces in adjacent lanes: whole sectors to and from memory, and a lane keeps its columns'
+    // scales and bias through a sub-tile, its rows' scales through a tile.
+    constexpr int kCols = kGated ? 16 : 32, kWide = kF32 ? 4 : 8, kPieces = kCols / kWide, kRows = 32 / kPieces;
+    const uint32_t buf = sbase + kW8Out + ew * kW8StageOut;
     float* sw_s = reinterpret_cast<float*>(smem + kW8Vec) + ew * 256;  // [4 sub-tiles][32]
     float* bias_s = sw_s + 128;
-    int stores = 0;
+    const int subs = tile_n / kCols;  // a tile's sub-tiles; this warp's: half, half + 2, ...
+    const int lrow = lane * kWide / kCols, lcol = lane * kWide % kCols;
+    using Out = std::conditional_t<kF32, float, __nv_bfloat16>;
+    const Out* residual = static_cast<const Out*>(p.residual);
+    Out* out = static_cast<Out*>(p.Y);
+    const bool add = !kGated && p.residual != nullptr;
+    auto first_row = [&](int m0) { return m0 + kW8BM * static_cast<int>(rank) + quad * 32; };
+    auto unit = [&](int row, int c) {  // 16-byte unit c of a row, in this warp's buffer
+      return kGated ? buf + row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : buf + row * 128 + ((c ^ (row & 7)) << 4);
+    };
+    // scales and bias of this warp's columns, scales of the lane's rows: read a tile ahead
+    float nsw[4], nbias[4], nsa[kPieces];
+    auto read_scales = [&](int i) {
+      int m0, n0;
+      tile_mn(i, m0, n0);
+      const int mrow = first_row(m0);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int m = mrow + k * kRows + lrow;
+        nsa[k] = m < p.M ? p.a_scale[m] : 0.0f;
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int oc = n0 + (2 * t + half) * kCols + lane % kCols;
+        const int row = kGated && lane >= 16 ? p.N + oc : oc;
+        const bool in = 2 * t + half < subs && oc < p.N;
+        nsw[t] = in ? p.w_scale[row] : 0.0f;
+        nbias[t] = in && p.bias != nullptr ? __bfloat162float(p.bias[row]) : 0.0f;
+      }
+      if (add && mrow + lane < p.M)
+        for (int t = half; t < subs && n0 + t * 32 < p.N; t += 2)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(residual + static_cast<size_t>(mrow + lane) * p.ldr + n0 + t * 32));
+    };
+    uint4 res[kPieces];  // the residual of a sub-tile, read one sub-tile ahead
+    auto read_residual = [&](int mrow, int n) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int m = mrow + k * kRows + lrow;
+        if (m < p.M && n + lcol < p.N)
+          res[k] = *reinterpret_cast<const uint4*>(residual + static_cast<size_t>(m) * p.ldr + n + lcol);
+      }
+    };
     bool ok = true;
+    if (my_tiles > 0) {
+      read_scales(0);
+      int m0, n0;
+      tile_mn(0, m0, n0);
+      if (add && half < subs) read_residual(first_row(m0), n0 + half * kCols);
+    }
     for (int i = 0; i < my_tiles && ok; ++i) {
       int m0, n0;
       tile_mn(i, m0, n0);
-      const int mrow = m0 + kW8BM * static_cast<int>(rank) + quad * 32;
-      const int m = mrow + lane;
-      const float sa = m < p.M ? p.a_scale[m] : 0.0f;
-      // scales and bias of this warp's 32-column sub-tiles; gated, the up rows' 64 further on
+      const int mrow = first_row(m0);
+      float sa[kPieces];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) sa[k] = nsa[k];
       __syncwarp();
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int oc = n0 + (2 * (kGated ? t & 1 : t) + half) * 32 + lane;
-        const bool in = oc < p.N;
-        const int row = kGated && t >= 2 ? p.N + oc : oc;
-        sw_s[t * 32 + lane] = in ? p.w_scale[row] : 0.0f;
-        bias_s[t * 32 + lane] = in && p.bias != nullptr ? __bfloat162float(p.bias[row]) : 0.0f;
+        sw_s[t * 32 + lane] = nsw[t];
+        bias_s[t * 32 + lane] = nbias[t];
       }
-      __syncwarp();
+      if (i + 1 < my_tiles) read_scales(i + 1);
       ok = mbar_wait(bar_acc_full(i & 1), (i >> 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -240,107 +310,95 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(lead(bar_acc_free(i & 1)));
       };
-      auto finish = [&](const uint32_t (&acc)[32], int t, float (&z)[32]) {
-        const float4* sv = reinterpret_cast<const float4*>(sw_s + t * 32);
-        const float4* bv = reinterpret_cast<const float4*>(bias_s + t * 32);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 s4 = sv[q], b4 = bv[q];
-          z[4 * q + 0] = fmaf(__uint_as_float(acc[4 * q + 0]) * sa, s4.x, b4.x);
-          z[4 * q + 1] = fmaf(__uint_as_float(acc[4 * q + 1]) * sa, s4.y, b4.y);
-          z[4 * q + 2] = fmaf(__uint_as_float(acc[4 * q + 2]) * sa, s4.z, b4.z);
-          z[4 * q + 3] = fmaf(__uint_as_float(acc[4 * q + 3]) * sa, s4.w, b4.w);
-        }
-      };
-      auto store_sub = [&](float (&y)[32], int n) {
-        if (p.residual != nullptr && m < p.M) {
-          if (p.out_f32) {
-            const float* r = static_cast<const float*>(p.residual) + static_cast<size_t>(m) * p.ldr + n;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              if (n + 4 * c < p.N) {
-                const float4 v = *reinterpret_cast<const float4*>(r + 4 * c);
-                y[4 * c] += v.x; y[4 * c + 1] += v.y; y[4 * c + 2] += v.z; y[4 * c + 3] += v.w;
-              }
-          } else {
-            const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.residual) + static_cast<size_t>(m) * p.ldr + n;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (n + 8 * c < p.N) {
-                const uint4 v = *reinterpret_cast<const uint4*>(r + 8 * c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  y[8 * c + 2 * j] += __uint_as_float(w[j] << 16);
-                  y[8 * c + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-                }
-              }
-          }
-        }
-        uint32_t buf;
-        if (p.out_f32) {
-          buf = out_buf;  // one 4 KB buffer, rows of 128 B, 128-byte swizzle
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             buf + lane * 128 + ((c ^ (lane & 7)) << 4)),
-                         "f"(y[4 * c]), "f"(y[4 * c + 1]), "f"(y[4 * c + 2]), "f"(y[4 * c + 3])
-                         : "memory");
-        } else {
-          buf = out_buf + (stores & 1) * 2048;  // two 2 KB buffers, rows of 64 B, 64-byte swizzle
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-            pk[j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
-                         "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
-                         : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&tm_y, buf, n, mrow);
-          bulk_commit();
-        }
-        ++stores;
-      };
-      const int subs = tile_n / 32;  // the tile's sub-tiles; this warp's: half, half + 2, ...
       if (half >= subs) release();
 #pragma unroll 1
       for (int t = half; t < subs; t += 2) {
         uint32_t acc[32];
-        tmem_ld32(t_row + t * 32, acc);
-        uint32_t up[kGated ? 32 : 1];
-        if constexpr (kGated) tmem_ld32(t_row + half_n + t * 32, up);
+        if constexpr (kGated) tmem_ld16x2(t_row + t * 16, t_row + half_n + t * 16, acc);
+        else tmem_ld32(t_row + t * 32, acc);
         tmem_ld_wait();
         if (t + 2 >= subs) release();
-        const int n = n0 + t * 32;
-        if (n >= p.N || mrow >= p.M) continue;  // warp-uniform
-        float y[32];
-        finish(acc, t >> 1, y);
-        if (p.act != kW8ActNone) {
+        __syncwarp();  // the sub-tile before has been read
 #pragma unroll
-          for (int q = 0; q < 32; ++q) y[q] = w8_act(y[q], p.act);
-        }
-        if constexpr (kGated) {
-          float u[32];
-          finish(up, 2 + (t >> 1), u);
+        for (int c = 0; c < 8; ++c)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(kGated ? unit(lane, c & 3) + (c >> 2) * 2048 : unit(lane, c)),
+                       "r"(acc[4 * c]), "r"(acc[4 * c + 1]), "r"(acc[4 * c + 2]), "r"(acc[4 * c + 3])
+                       : "memory");
+        __syncwarp();
+        const int n = n0 + t * kCols;
+        if (n < p.N && mrow < p.M) {  // warp-uniform
+          const float* swp = sw_s + (t >> 1) * 32 + lcol;
+          const float* bp = bias_s + (t >> 1) * 32 + lcol;
+          float4 sw[kWide / 4], bias[kWide / 4], usw[kWide / 4], ubias[kWide / 4];
 #pragma unroll
-          for (int q = 0; q < 32; ++q) y[q] *= u[q];
+          for (int q = 0; q < kWide / 4; ++q) {
+            sw[q] = reinterpret_cast<const float4*>(swp)[q];
+            bias[q] = reinterpret_cast<const float4*>(bp)[q];
+            if (kGated) {
+              usw[q] = reinterpret_cast<const float4*>(swp + 16)[q];
+              ubias[q] = reinterpret_cast<const float4*>(bp + 16)[q];
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) {
+            const int row = k * kRows + lrow, m = mrow + row;
+            const float2 s2 = make_float2(sa[k], sa[k]);
+            float2 y[kWide / 2];
+#pragma unroll
+            for (int q = 0; q < kWide / 4; ++q) {
+              const float4 v = lds_f4(unit(row, lcol / 4 + q));
+              y[2 * q] = __ffma2_rn(__fmul2_rn(make_float2(v.x, v.y), s2), make_float2(sw[q].x, sw[q].y),
+                                    make_float2(bias[q].x, bias[q].y));
+              y[2 * q + 1] = __ffma2_rn(__fmul2_rn(make_float2(v.z, v.w), s2), make_float2(sw[q].z, sw[q].w),
+                                        make_float2(bias[q].z, bias[q].w));
+            }
+            if (p.act != kW8ActNone) {
+#pragma unroll
+              for (int q = 0; q < kWide / 2; ++q) y[q] = make_float2(w8_act(y[q].x, p.act), w8_act(y[q].y, p.act));
+            }
+            if constexpr (kGated) {
+#pragma unroll
+              for (int q = 0; q < kWide / 4; ++q) {
+                const float4 v = lds_f4(unit(row, lcol / 4 + q) + 2048);
+                y[2 * q] = __fmul2_rn(y[2 * q], __ffma2_rn(__fmul2_rn(make_float2(v.x, v.y), s2), make_float2(usw[q].x, usw[q].y),
+                                                           make_float2(ubias[q].x, ubias[q].y)));
+                y[2 * q + 1] = __fmul2_rn(y[2 * q + 1], __ffma2_rn(__fmul2_rn(make_float2(v.z, v.w), s2), make_float2(usw[q].z, usw[q].w),
+                                                                   make_float2(ubias[q].z, ubias[q].w)));
+              }
+            }
+            uint32_t w[4];
+            if constexpr (kF32) {
+              if (add) {
+                y[0] = __fadd2_rn(y[0], make_float2(__uint_as_float(res[k].x), __uint_as_float(res[k].y)));
+                y[1] = __fadd2_rn(y[1], make_float2(__uint_as_float(res[k].z), __uint_as_float(res[k].w)));
+              }
+              w[0] = __float_as_uint(y[0].x); w[1] = __float_as_uint(y[0].y);
+              w[2] = __float_as_uint(y[1].x); w[3] = __float_as_uint(y[1].y);
+            } else {
+              const uint32_t r4[4] = {res[k].x, res[k].y, res[k].z, res[k].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (add)
+                  y[q] = __fadd2_rn(y[q], make_float2(__uint_as_float(r4[q] << 16), __uint_as_float(r4[q] & 0xFFFF0000u)));
+                const __nv_bfloat162 b2 = __float22bfloat162_rn(y[q]);
+                w[q] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+            }
+            if (m < p.M && n + lcol < p.N)
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(m) * p.ldy + n + lcol) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-        store_sub(y, n);
+        if (add) {
+          if (t + 2 < subs) {
+            read_residual(mrow, n + 2 * kCols);
+          } else if (i + 1 < my_tiles) {
+            int m1, n1;
+            tile_mn(i + 1, m1, n1);
+            read_residual(first_row(m1), n1 + half * kCols);
+          }
+        }
       }
     }
-    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
