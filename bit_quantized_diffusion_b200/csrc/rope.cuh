@@ -16,6 +16,8 @@
 // left out are below 2^-29).
 #pragma once
 
+#include <type_traits>
+
 #include "sm100.cuh"
 
 namespace svdq {
@@ -262,9 +264,10 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
 }
 
 // cos, sin as [M, P]: a thread keeps V adjacent pairs, their fractions in registers, and
-// walks down the rows, four at a time; pairs of one axis (most are) read its position once.
-// 131072 rows of 64 pairs, 67.6 MB: 14.8 us, 4.6 TB/s, the stores sharing the time with 25
-// instructions an angle (40.4 us with sincospi of a float64 angle's fraction).
+// walks down the rows, four at a time. Its pairs' positions: one per row where there is one
+// axis, two where its pairs lie on two (so that no lane of a warp takes another way), else one
+// per pair. 131072 rows of 64 pairs, 67.6 MB: 14.8 us, 4.6 TB/s, the stores sharing the time
+// with 25 instructions an angle (40.4 us with sincospi of a float64 angle's fraction).
 template <int V, typename Pos>
 __global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) {
   const int nq = p.P / V, per_row = min(nq, 256), rows = 256 / per_row;
@@ -275,11 +278,14 @@ __global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) 
   const Pos* positions = static_cast<const Pos*>(p.positions);
   for (int q = threadIdx.x % per_row; q < nq; q += per_row) {
     RopePair pair[V];
-    bool one = true;
+    bool two = true;
+    uint32_t last = 0;  // bit j: pair j lies on the last pair's axis
+#pragma unroll
+    for (int j = 0; j < V; ++j) pair[j] = rope_pair(p, q * V + j);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      pair[j] = rope_pair(p, q * V + j);
-      one = one && pair[j].axis == pair[0].axis;
+      if (pair[j].axis == pair[V - 1].axis) last |= 1u << j;
+      else two = two && pair[j].axis == pair[0].axis;
     }
     const size_t step = static_cast<size_t>(gridDim.x) * rows;
     auto put = [&](size_t m, const Pos (&pos)[V]) {
@@ -304,22 +310,31 @@ __global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) 
       *reinterpret_cast<RopeVec<float, V>*>(p.sin + m * p.P + q * V) = s;
     };
     size_t m = static_cast<size_t>(blockIdx.x) * rows + r;
-    if (one) {
-      const Pos* at = positions + pair[0].axis;
+    // kPos positions per row, of the first pair and of the last
+    auto walk = [&](auto count) {
+      constexpr int kPos = decltype(count)::value;
       for (; m < p.M; m += 4 * step) {
-        Pos four[4];
+        Pos four[4][kPos];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (m + k * step < p.M) four[k] = __ldg(at + (m + k * step) * p.A);
+          if (m + k * step < p.M) {
+            four[k][0] = __ldg(positions + (m + k * step) * p.A + pair[0].axis);
+            if (kPos > 1) four[k][kPos - 1] = __ldg(positions + (m + k * step) * p.A + pair[V - 1].axis);
+          }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (m + k * step >= p.M) break;
           Pos pos[V];
 #pragma unroll
-          for (int j = 0; j < V; ++j) pos[j] = four[k];
+          for (int j = 0; j < V; ++j) pos[j] = kPos > 1 && (last >> j & 1) ? four[k][kPos - 1] : four[k][0];
           put(m + k * step, pos);
         }
       }
+    };
+    if (p.A == 1 || V == 1) {
+      walk(std::integral_constant<int, 1>());
+    } else if (two) {
+      walk(std::integral_constant<int, 2>());
     } else {
       for (; m < p.M; m += step) {
         Pos pos[V];
@@ -331,26 +346,31 @@ __global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) 
   }
 }
 
-// cos, sin as [P, M]: neighbouring threads take neighbouring rows, a block up to
-// kRopeTablePairs pairs.
+// cos, sin as [P, M]: neighbouring threads take neighbouring rows, a block kRopeTablePairs
+// pairs, whose fractions are made once, in shared memory (100000 rows of 64 pairs, 51.6 MB: 14.3 us).
 constexpr int kRopeTablePairs = 8;
 __global__ void __launch_bounds__(256) rope_table_angle_major_kernel(const RopeParams p) {
-  const size_t m = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  __shared__ RopePair pairs[kRopeTablePairs];
+  const int i0 = blockIdx.y * kRopeTablePairs, n = min(p.P - i0, kRopeTablePairs);
   grid_dep_wait();
   grid_dep_launch();
-  if (m >= p.M) return;
-  const int end = min(p.P, static_cast<int>(blockIdx.y + 1) * kRopeTablePairs);
-#pragma unroll 4
-  for (int i = blockIdx.y * kRopeTablePairs; i < end; i += 2) {
-    const RopePair a = rope_pair(p, i), b = i + 1 < end ? rope_pair(p, i + 1) : a;
-    float2 c, s;
-    rope_cos_sin2(rope_turn(rope_position(p, m, a.axis), a.fraction), rope_turn(rope_position(p, m, b.axis), b.fraction),
-                  make_float2(a.scale, b.scale), c, s);
-    p.cos[static_cast<size_t>(i) * p.M + m] = c.x;
-    p.sin[static_cast<size_t>(i) * p.M + m] = s.x;
-    if (i + 1 < end) {
-      p.cos[static_cast<size_t>(i + 1) * p.M + m] = c.y;
-      p.sin[static_cast<size_t>(i + 1) * p.M + m] = s.y;
+  if (threadIdx.x < kRopeTablePairs) pairs[threadIdx.x] = rope_pair(p, i0 + min(static_cast<int>(threadIdx.x), n - 1));
+  __syncthreads();
+  for (size_t m = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; m < p.M; m += static_cast<size_t>(gridDim.x) * 256) {
+#pragma unroll
+    for (int j = 0; j < kRopeTablePairs; j += 2) {
+      if (j >= n) break;
+      const RopePair a = pairs[j], b = pairs[j + 1];
+      float2 c, s;
+      rope_cos_sin2(rope_turn(rope_position(p, m, a.axis), a.fraction), rope_turn(rope_position(p, m, b.axis), b.fraction),
+                    make_float2(a.scale, b.scale), c, s);
+      const size_t at = static_cast<size_t>(i0 + j) * p.M + m;
+      p.cos[at] = c.x;
+      p.sin[at] = s.x;
+      if (j + 1 < n) {
+        p.cos[at + p.M] = c.y;
+        p.sin[at + p.M] = s.y;
+      }
     }
   }
 }

@@ -1153,26 +1153,43 @@ svdq_status launch_w8a8_gemv(const DeviceInfo* d, bool gated, const W8Params& q,
   return launch_status();
 }
 
-// The 8-bit linear of at most kWsMaxT tokens: one cluster of `splits` CTAs per tile of
-// 128 weight rows, the smallest power of two (at most 8, at most half the K tiles) that
-// gives four in five SMs a CTA (77 tokens, K = 3840: N = 3840 takes 14.7, 11.1, 9.2, 10.9 us
-// with 1, 2, 4, 8; N = 15360 17.7, 17.7, 23.9). More CTAs than SMs share them two by two.
-svdq_status launch_w8a8_stream(const DeviceInfo* d, bool gated, const W8Params& q, const void* a_codes,
-                               const void* w_codes, void* Y, int ldy, svdq_stream_t stream) {
+// How the streaming kernel takes a product: token tiles of T, and a cluster of `splits` CTAs
+// per tile of 128 weight rows, the smallest power of two (at most 8, at most half the K
+// tiles) that gives four in five SMs a CTA (77 tokens, K = 3840: N = 3840 takes 14.7, 11.1, 9.2, 10.9 us
+// with 1, 2, 4, 8; N = 15360 17.7, 17.7, 23.9).
+struct StreamPlan {
+  long long tiles;             // of weight rows
+  int token_tiles, T, ktiles, splits;
+};
+StreamPlan stream_plan(const DeviceInfo* d, bool gated, int M, int N, int K) {
+  StreamPlan s;
+  const int tile_n = gated ? 64 : 128;
+  s.tiles = (static_cast<long long>(N) + tile_n - 1) / tile_n;
+  s.token_tiles = (M + kWsMaxT - 1) / kWsMaxT;
+  s.T = ((M + s.token_tiles - 1) / s.token_tiles + 15) / 16 * 16;
+  s.ktiles = (K + kW8KStage - 1) / kW8KStage;
+  s.splits = 1;
+  while (s.splits < 8 && 2 * s.splits <= s.ktiles && 5 * s.tiles * s.token_tiles * s.splits < 4ll * d->num_sms)
+    s.splits *= 2;
+  return s;
+}
+
+// More CTAs than SMs share them two by two.
+svdq_status launch_w8a8_stream(const DeviceInfo* d, bool gated, const W8Params& q, const StreamPlan& plan,
+                               const void* a_codes, const void* w_codes, void* Y, int ldy, svdq_stream_t stream) {
   WsParams p;
   p.M = q.M;
   p.N = q.N;
   p.K = q.K;
-  p.T = (q.M + 15) / 16 * 16;
+  p.T = plan.T;
   p.tb = p.T <= 32 ? 32 : (p.T <= 64 ? 64 : 128);
-  const int tile_n = gated ? 64 : 128, tiles = (q.N + tile_n - 1) / tile_n;
-  const int ktiles = (q.K + kW8KStage - 1) / kW8KStage;
-  if (tiles > INT32_MAX / 8) return SVDQ_ERR_UNSUPPORTED;
-  int splits = 1;
-  while (splits < 8 && 2 * splits <= ktiles && 5ll * tiles * splits < 4ll * d->num_sms) splits *= 2;
+  const int splits = plan.splits, ktiles = plan.ktiles;
+  if (plan.tiles > INT32_MAX / 8 || plan.token_tiles > 65535) return SVDQ_ERR_UNSUPPORTED;
+  const int tiles = static_cast<int>(plan.tiles);
   p.splits = splits;
-  p.shared = tiles * splits > d->num_sms;
-  const size_t budget = p.shared ? 113 * 1024 : 226 * 1024;
+  p.shared = plan.tiles * plan.token_tiles * splits > d->num_sms;
+  // two CTAs to an SM also for the widest clusters: few of eight whole SMs each find room at once
+  const size_t budget = p.shared || splits == 8 ? 113 * 1024 : 226 * 1024;
   const int per_cta = (ktiles + splits - 1) / splits;
   int stages = kWsMaxStages;
   while (stages > 2 && (ws_smem_bytes(p.T, stages) > budget || stages > per_cta)) --stages;
@@ -1195,7 +1212,7 @@ svdq_status launch_w8a8_stream(const DeviceInfo* d, bool gated, const W8Params& 
     return SVDQ_ERR_CUDA;
   auto kern = gated ? (splits > 1 ? w8a8_stream_kernel<true, true> : w8a8_stream_kernel<true, false>)
                     : (splits > 1 ? w8a8_stream_kernel<false, true> : w8a8_stream_kernel<false, false>);
-  if (launch_kernel(d, kern, dim3(tiles * splits), dim3(kWsThreads), ws_smem_bytes(p.T, stages),
+  if (launch_kernel(d, kern, dim3(tiles * splits, plan.token_tiles), dim3(kWsThreads), ws_smem_bytes(p.T, stages),
                     static_cast<cudaStream_t>(stream), splits, tm_w, tm_x, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return SVDQ_ERR_CUDA;
@@ -1247,10 +1264,9 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   // tile's K, or K is long: the sum over a cluster grows with the tokens (128 tokens: K = N = 1024
   // 6.5 / 5.2, K = 2048, N = 3840 9.1 / 8.4, K = N = 3840 10.8 / 10.6, K = 1024, N = 15360 12.7 / 12.9,
   // K = 15360, N = 3840 18.2 / 26.4).
-  const int tile_rows = gated ? 64 : 128;
-  const bool unsplit = 5ll * ((N + tile_rows - 1) / tile_rows) >= 4ll * d->num_sms;
-  if (M <= 64 || (M <= kWsMaxT && (unsplit || K >= 3500)))
-    return launch_w8a8_stream(d, gated, p, a_codes, w_codes, Y, ldy, stream);
+  const StreamPlan plan = stream_plan(d, gated, M, N, K);
+  if (M <= 64 || (M <= kWsMaxT && (plan.splits == 1 || K >= 3500)))
+    return launch_w8a8_stream(d, gated, p, plan, a_codes, w_codes, Y, ldy, stream);
   // The tile's width: the one whose waves of tiles over the CTA pairs take least, a stage
   // of K costing its operands' way in, 256 + bn rows per pair (at 256 columns that equals its
   // MMA time). K = 3840: M = 256, N = 3840 takes 10.7 us at 64 columns and 18.4 at 256, M = 4608
@@ -1269,6 +1285,16 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
     }
   }
   if (best < 0) return SVDQ_ERR_UNSUPPORTED;
+  // A long K over few tiles leaves most pairs idle, while clusters that split K reach every SM. Both
+  // sides in clocks: the operands' way in, and, for the clusters, the sum over them and, past eight
+  // of the widest, their waiting for whole groups of SMs (M, K, N = 340, 12512, 64: 9.1 us against
+  // 18.9 in pairs; 512, 15360, 256: 12.3 and 21.6; 256, 15360, 3840: 29.1 and 27.2; 200, 4096, 1024: 9.7
+  // and 8.5).
+  const long long clusters = plan.tiles * plan.token_tiles;
+  const long long split_cost = (plan.ktiles + plan.splits - 1) / plan.splits * (128ll + plan.T) * 3 + 3000 +
+                               (plan.splits == 8 && clusters > 8 ? 5000 : 0);
+  if (plan.splits > 1 && split_cost < best * plan.ktiles)
+    return launch_w8a8_stream(d, gated, p, plan, a_codes, w_codes, Y, ldy, stream);
   p.tiles_m = static_cast<int>(tiles_m);
   // Row tiles in bands whose rows of A stay in a part of L2 while the weight passes by:
   // the weight is read once per band, A once. (M, K, N) = (4096, 15360, 3840), A 63 MB: two
@@ -1482,8 +1508,9 @@ svdq_status svdq_rope_table(int M, int pairs, int axes, const void* positions, i
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (angle_major) {
-    e = launch_kernel(d, rope_table_angle_major_kernel,
-                      dim3((M - 1) / 256 + 1, (pairs + kRopeTablePairs - 1) / kRopeTablePairs), dim3(256), 0, cs, 1, p);
+    const int across = (pairs + kRopeTablePairs - 1) / kRopeTablePairs, wanted = (8 * d->num_sms + across - 1) / across;
+    const int down = (M - 1) / 256 + 1;
+    e = launch_kernel(d, rope_table_angle_major_kernel, dim3(down < wanted ? down : wanted, across), dim3(256), 0, cs, 1, p);
   } else {
     // four pairs per thread and 16-byte stores where rows keep that alignment
     const bool wide = pairs % 4 == 0 && aligned16(cos) && aligned16(sin);

@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   }
 }
 
-// w8a8_stream_kernel: up to 128 tokens, where the product is bound by reading the
-// weight once. The operands change sides: 128 weight rows are the MMA's M (tensor-memory
+// w8a8_stream_kernel: up to 128 tokens (or tiles of as many, where a long K meets few
+// columns), where the product is bound by reading the weight once. The operands change sides: 128 weight rows are the MMA's M (tensor-memory
 // lanes), the tokens, rounded up to 16, its N, so a handful of tokens costs no padding
 // to 256 rows. One tile of 128 weight rows (gated: 64 gate rows and the 64 matching up
 // rows) per cluster, whose CTAs split K and add their float32 partial sums through
@@ -431,7 +431,7 @@ constexpr int kWsMaxStages = 12;
 
 struct WsParams {
   int M, N, K;                 // N: output columns (F when gated)
-  int T, tb;                   // tokens rounded up to 16; tensor-memory columns (32, 64, 128)
+  int T, tb;                   // tokens per tile, a multiple of 16; tensor-memory columns (32, 64, 128)
   int splits, stages;          // cluster size; pipeline stages
   int shared;                  // more CTAs than SMs: two on one
   int act, out_f32;
@@ -512,6 +512,8 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   const int tile = blockIdx.x / splits;
   constexpr int kCols = kGated ? 64 : 128;      // output columns per tile
   const int n0 = tile * kCols;
+  // this tile's tokens; more than one tile only where K is split
+  const int m0 = kSplit ? blockIdx.y * T : 0, rows = kSplit ? min(T, p.M - m0) : p.M;
   const int ktiles = (p.K + kW8KStage - 1) / kW8KStage;
   const int k0 = rank * ktiles / splits, k1 = (rank + 1) * ktiles / splits;
 
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
     mbar_arrive_expect_tx(bar_full(s), SB);
     tma_load_2d(st, &tm_w, bar_full(s), kt * kW8KStage, n0);
     tma_load_2d(st + 64 * 128, &tm_w, bar_full(s), kt * kW8KStage, kGated ? p.N + n0 : n0 + 64);
-    tma_load_2d(st + 128 * 128, &tm_x, bar_full(s), kt * kW8KStage, 0);
+    tma_load_2d(st + 128 * 128, &tm_x, bar_full(s), kt * kW8KStage, m0);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   // steps of the block, which keep a thread at the same columns; their scales and bias now
   constexpr int kQuads = kCols / 4, kStep = kSplit ? 1 : (kGated ? 2 : 4);
   static_assert(kWsThreads % kQuads == 0, "a thread keeps its columns");
-  const int items = p.M * kQuads;
+  const int items = rows * kQuads;
   const int e1 = (rank + 1) * items / splits;
   int e = rank * items / splits + static_cast<int>(threadIdx.x);
   const int c = 4 * (e % kQuads), n = n0 + c;
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
 #pragma unroll
     for (int j = 0; j < kStep; ++j)
       if (p.residual != nullptr && n < p.N && from + j * kWsThreads < e1)
-        w8_load4(p.residual, static_cast<size_t>((from + j * kWsThreads) / kQuads) * p.ldr + n, p.out_f32, r[j]);
+        w8_load4(p.residual, static_cast<size_t>(m0 + (from + j * kWsThreads) / kQuads) * p.ldr + n, p.out_f32, r[j]);
   };
   residual(e);
   // the cluster's four sums of row m from accumulator column col, in rank order
@@ -616,15 +618,15 @@ __global__ void __launch_bounds__(kWsThreads, 2)
     }
   } else {
     const int quad = warp & 3;
-    for (int i = threadIdx.x - 64; i < p.M; i += kWsThreads - 64) sa_s[i] = p.a_scale[i];
+    for (int i = threadIdx.x - 64; i < rows; i += kWsThreads - 64) sa_s[i] = p.a_scale[m0 + i];
     if (p.residual != nullptr) {
       // the rest of the residual: read at the very end, from memory it would add a latency per step
       const int esz = p.out_f32 ? 4 : 2, lines = kCols * esz / 128;
-      for (int i = threadIdx.x - 64; i < p.M * lines; i += kWsThreads - 64) {
+      for (int i = threadIdx.x - 64; i < rows * lines; i += kWsThreads - 64) {
         const int col = n0 + (i % lines) * (128 / esz);
         if (col < p.N)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p.residual) +
-                                                        (static_cast<size_t>(i / lines) * p.ldr + col) * esz));
+                                                        (static_cast<size_t>(m0 + i / lines) * p.ldr + col) * esz));
       }
     }
     // the stages' memory is free once the last MMA is done
@@ -689,7 +691,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
 #pragma unroll
       for (int j = 0; j < kStep; ++j)
         if (e + j * kWsThreads < e1)
-          w8_store4(p.Y, static_cast<size_t>((e + j * kWsThreads) / kQuads) * p.ldy + n, p.out_f32, y[j]);
+          w8_store4(p.Y, static_cast<size_t>(m0 + (e + j * kWsThreads) / kQuads) * p.ldy + n, p.out_f32, y[j]);
     }
   }
   // peers read this CTA's sums until here

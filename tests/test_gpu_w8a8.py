@@ -167,6 +167,7 @@ CASES = [  # M, N, K, bias, act, residual: every kernel (few tokens of a small w
     # without K shared by a cluster, CTA pairs of several widths), each at ragged sizes
     (1, 4752, 272, True, None, True), (3, 272, 4112, True, "silu", True), (8, 4736, 4096, True, None, False),
     (9, 160, 2048, False, None, True), (13, 15360, 144, True, "gelu", True), (16, 80, 2064, True, None, True),
+    (340, 64, 12512, True, "gelu", True), (1000, 48, 4112, True, None, True), (130, 272, 4096, False, "silu", True),
     (100, 15376, 80, False, None, True), (128, 272, 3504, True, "silu", False),
     (1, 16, 16, False, None, False), (1, 3840, 512, True, None, True), (2, 48, 4096, True, "silu", True),
     (7, 1040, 784, False, "gelu", False), (16, 272, 3856, True, None, False), (17, 128, 144, True, "gelu", True),
@@ -215,7 +216,7 @@ def test_linear_is_exact_on_whole_numbers(bq, M):
 @TYPES
 @pytest.mark.parametrize("M,F,K,bias,act", [
     (1, 2384, 272, True, "silu"), (8, 2368, 4096, False, "silu"), (9, 80, 2048, True, "gelu"), (12, 80, 2064, False, "silu"),
-    (100, 10256, 80, False, "silu"), (1, 16, 16, False, "silu"), (1, 1040, 3840, False, "silu"), (4, 272, 1040, True, "silu"), (16, 64, 4112, True, "gelu"),
+    (199, 96, 1680, True, "silu"), (500, 64, 8208, False, "gelu"), (100, 10256, 80, False, "silu"), (1, 16, 16, False, "silu"), (1, 1040, 3840, False, "silu"), (4, 272, 1040, True, "silu"), (16, 64, 4112, True, "gelu"),
     (31, 400, 144, False, "silu"), (64, 528, 2048, True, None), (128, 80, 512, False, "gelu"), (130, 272, 656, True, "silu"),
     (300, 464, 384, True, "gelu"), (600, 1040, 256, False, "silu")])
 def test_gated_linear(bq, M, F, K, bias, act, dtype):
