@@ -1160,6 +1160,7 @@ svdq_status launch_w8a8_gemv(const DeviceInfo* d, bool gated, const W8Params& q,
 struct StreamPlan {
   long long tiles;             // of weight rows
   int token_tiles, T, ktiles, splits;
+  bool full;                   // tiles enough without splitting
 };
 StreamPlan stream_plan(const DeviceInfo* d, bool gated, int M, int N, int K) {
   StreamPlan s;
@@ -1168,6 +1169,7 @@ StreamPlan stream_plan(const DeviceInfo* d, bool gated, int M, int N, int K) {
   s.token_tiles = (M + kWsMaxT - 1) / kWsMaxT;
   s.T = ((M + s.token_tiles - 1) / s.token_tiles + 15) / 16 * 16;
   s.ktiles = (K + kW8KStage - 1) / kW8KStage;
+  s.full = 5 * s.tiles * s.token_tiles >= 4ll * d->num_sms;
   s.splits = 1;
   while (s.splits < 8 && 2 * s.splits <= s.ktiles && 5 * s.tiles * s.token_tiles * s.splits < 4ll * d->num_sms)
     s.splits *= 2;
@@ -1260,12 +1262,12 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   if (M <= kWvMaxM && K <= (M <= 8 ? 4096 : 2048) && N / (gated ? 8 : 16) <= 2 * d->num_sms)
     return launch_w8a8_gemv(d, gated, p, a_codes, w_codes, Y, ldy, stream);
   // Few tokens stream the weight (64 tokens, streamed / in CTA pairs: K = N = 1024 5.0 / 4.8 us,
-  // K = N = 3840 8.8 / 10.1, K = 1024, N = 15360 9.9 / 12.1). Above 64 only where no CTA shares a
-  // tile's K, or K is long: the sum over a cluster grows with the tokens (128 tokens: K = N = 1024
+  // K = N = 3840 8.8 / 10.1, K = 1024, N = 15360 9.9 / 12.1). Above 64 only where the tiles
+  // suffice without sharing K, or K is long: the sum over a cluster grows with the tokens (128 tokens: K = N = 1024
   // 6.5 / 5.2, K = 2048, N = 3840 9.1 / 8.4, K = N = 3840 10.8 / 10.6, K = 1024, N = 15360 12.7 / 12.9,
   // K = 15360, N = 3840 18.2 / 26.4).
   const StreamPlan plan = stream_plan(d, gated, M, N, K);
-  if (M <= 64 || (M <= kWsMaxT && (plan.splits == 1 || K >= 3500)))
+  if (M <= 64 || (M <= kWsMaxT && (plan.full || K >= 3500)))
     return launch_w8a8_stream(d, gated, p, plan, a_codes, w_codes, Y, ldy, stream);
   // The tile's width: the one whose waves of tiles over the CTA pairs take least, a stage
   // of K costing its operands' way in, 256 + bn rows per pair (at 256 columns that equals its
