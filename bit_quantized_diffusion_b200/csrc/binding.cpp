@@ -100,7 +100,8 @@ struct Heads {
   int ld, ldh;
   Heads(const Tensor& t, at::IntArrayRef shape, ScalarType type, const Place& p, const char* name) {
     check(t, shape, type, p, name);
-    const int64_t h = shape[1] > 1 ? t.stride(1) : shape[2], m = shape[0] > 1 ? t.stride(0) : shape[1] * h;
+    // (one row or one head has no step to the next)
+    const int64_t h = shape[1] > 1 ? t.stride(1) : shape[2], m = shape[0] > 1 ? t.stride(0) : shape[2];
     TORCH_CHECK_VALUE(t.stride(2) == 1 && h >= 0 && m >= 0 && h <= kIntMax && m <= kIntMax, name,
                       ": heads must be contiguous, strides below 2^31");
     at = t.data_ptr();

@@ -212,3 +212,20 @@ def test_offsets_beyond_32_bits(bq):
     cos, sin = bq.svdq_rope_table(torch.arange(M, dtype=torch.int32, device="cuda"), freq)
     c, s = bq.svdq_rope_table(torch.arange(M - 3, M, dtype=torch.int32, device="cuda"), freq)
     assert torch.equal(cos[-3:], c) and torch.equal(sin[-3:], s)
+
+
+def test_one_row_of_heads_far_apart(bq):
+    """One token of a [heads, length, D] cache: its heads lie further apart than 2^31 / heads."""
+    H, L, D = 6, 3_400_000, 128
+    cache = torch.empty(H, L, D, dtype=BF, device="cuda")
+    cache[:, 1:4].zero_()
+    row = cache[:, 2:3].transpose(0, 1)
+    x = torch.randn(1, H, D, generator=torch.Generator().manual_seed(3)).to(BF).cuda()
+    assert row.stride(1) * H > 2 ** 31
+    pos, freq = torch.tensor([2], dtype=torch.int64, device="cuda"), torch.logspace(0, -3, 64, dtype=torch.float64).cuda()
+    want = bq.svdq_rope(x, pos, freq)
+    bq.svdq_rope(x, pos, freq, Y=row)
+    assert torch.equal(row, want) and not cache[:, 1].any() and not cache[:, 3].any()
+    row.copy_(x)
+    bq.svdq_rope(row, pos, freq, Y=row)
+    assert torch.equal(row, want)
