@@ -151,8 +151,8 @@ __device__ __forceinline__ void rope_turn_pairs(float (&a)[N], float (&b)[N], co
   }
 }
 
-// A pair's fraction, axis and scale. An axis that the positions do not have: scale NaN, and
-// axis 0 read.
+// A pair's fraction, axis and scale. A frequency that is not finite, or an axis that the
+// positions do not have: scale NaN, and axis 0 read for the latter.
 struct RopePair {
   uint64_t fraction;
   int axis;
@@ -161,7 +161,8 @@ struct RopePair {
 __device__ __forceinline__ RopePair rope_pair(const RopeParams& p, int i) {
   const int a = p.axis != nullptr ? p.axis[i] : 0;
   const bool there = a >= 0 && a < p.A;
-  return {rope_fraction(p.freq[i]), there ? a : 0, there ? p.scale : __int_as_float(0x7fffffff)};
+  const double f = p.freq[i];
+  return {rope_fraction(f), there ? a : 0, there && isfinite(f) ? p.scale : __int_as_float(0x7fffffff)};
 }
 
 // One block per (row, share of the heads). The row's angles go through shared memory once;

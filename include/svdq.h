@@ -512,7 +512,8 @@ svdq_status w8a8_gated_linear(int M, int F, int K, const void* a_codes, const fl
  *
  * positions  [M, axes] int32 or int64 (position_bytes 4 or 8), any value
  * freq       float64 [pairs], radians per position: the base's powers, with whatever
- *            scaling a longer context asks for already in them
+ *            scaling a longer context asks for already in them (one that is not finite
+ *            gives NaN in its pair)
  * axis       int32 [pairs], the position axis of each pair (0 <= axis < axes; any
  *            other value gives NaN in that pair), or NULL: axis 0 for all
  * scale      factor on both tables (1, or a longer context's attention factor), finite

@@ -229,3 +229,25 @@ def test_one_row_of_heads_far_apart(bq):
     row.copy_(x)
     bq.svdq_rope(row, pos, freq, Y=row)
     assert torch.equal(row, want)
+
+
+def test_frequencies_that_are_not_finite(bq):
+    """NaN in their own pairs, the other pairs as without them: the rotation and both tables."""
+    freq = torch.logspace(0, -3, 16, dtype=torch.float64)
+    odd = freq.clone()
+    odd[2], odd[7], odd[13] = math.inf, math.nan, -math.inf
+    lost = torch.zeros(16, dtype=torch.bool)
+    lost[[2, 7, 13]] = True
+    freq, odd, lost = freq.cuda(), odd.cuda(), lost.cuda()
+    pos = torch.tensor([0, 5, -9], dtype=torch.int32, device="cuda")
+    x = torch.randn(3, 2, 40, generator=torch.Generator().manual_seed(4)).cuda()
+    for interleaved in (False, True):
+        want, got = (bq.svdq_rope(x, pos, f, interleaved=interleaved) for f in (freq, odd))
+        turned = lost.repeat_interleave(2) if interleaved else lost.repeat(2)
+        columns = torch.cat([turned, torch.zeros(8, dtype=torch.bool, device="cuda")])
+        assert got[..., columns].isnan().all() and torch.equal(got[..., ~columns], want[..., ~columns])
+    for angle_major in (False, True):
+        for want, got in zip(bq.svdq_rope_table(pos, freq, angle_major=angle_major),
+                             bq.svdq_rope_table(pos, odd, angle_major=angle_major)):
+            want, got = (t.t() if angle_major else t for t in (want, got))
+            assert got[:, lost].isnan().all() and torch.equal(got[:, ~lost], want[:, ~lost])
