@@ -170,26 +170,35 @@ class AwqW4A16Linear:
 class RotaryEmbedding:
     """Rotary positions of heads: frequencies once (prep.rope_frequencies), then any rows'
     heads turned, or the tables of their angles. ``dims`` is the number of rotary columns,
-    or one number per position axis; ``interleaved`` pairs adjacent columns, otherwise
-    column i pairs with column i + (rotary columns) / 2."""
+    or one number per position axis (positions are then [M, axes]; with one axis also [M]);
+    ``interleaved`` pairs adjacent columns, otherwise column i pairs with column
+    i + (rotary columns) / 2."""
 
     def __init__(self, dims, base: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
                  factor: float = 1.0, original_length: int | None = None, device="cuda"):
         freq, axis, self.scale = prep.rope_frequencies(dims, base, scaling, factor, original_length)
         self.rot_dim = 2 * freq.numel()
+        self.axes = int(axis.max()) + 1
         self.interleaved = bool(interleaved)
         self.freq = freq.to(device)
-        # one axis: the library's default
-        self.axis = None if isinstance(dims, int) or len(dims) == 1 else axis.to(device)
+        self.axis = axis.to(device) if self.axes > 1 else None  # one axis: the library's default
+
+    def _check(self, positions: torch.Tensor):
+        # the library gives NaN on an axis that the positions do not have
+        if (positions.shape[1] if positions.dim() == 2 else 1) != self.axes:
+            raise ValueError(f"positions must be [M, {self.axes}]" + (" or [M]" if self.axes == 1 else "")
+                             + f", not {list(positions.shape)}")
 
     def tables(self, positions: torch.Tensor, angle_major: bool = False, cos=None, sin=None, stream=None):
         """(cos, sin) float32 [M, pairs], or [pairs, M] with angle_major (SvdqQkvNormRope's)."""
+        self._check(positions)
         return svdq_rope_table(positions, self.freq, axis=self.axis, scale=self.scale, angle_major=angle_major,
                                cos=cos, sin=sin, stream=stream)
 
     def forward(self, x: torch.Tensor, positions: torch.Tensor, y: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
         """x [M, heads, D] turned; y may be x."""
+        self._check(positions)
         return svdq_rope(x, positions, self.freq, axis=self.axis, scale=self.scale, interleaved=self.interleaved,
                          Y=y, stream=stream)
 

@@ -238,3 +238,19 @@ def test_qkv_layer_makes_its_tables_of_positions(monkeypatch):
                dict(rotary=L.RotaryEmbedding(64, interleaved=True, device="cpu"), positions=pos)):
         with pytest.raises(ValueError):
             layer(x, **kw)
+
+
+def test_rotary_layer_wants_a_position_per_axis(monkeypatch):
+    monkeypatch.setattr(L, "svdq_rope_table", lambda pos, *a, **k: "tables")
+    monkeypatch.setattr(L, "svdq_rope", lambda x, *a, **k: "turned")
+    three, one, tuple_of_one = (L.RotaryEmbedding(d, device="cpu") for d in ((16, 24, 24), 64, (64,)))
+    x = torch.zeros(5, 2, 64, dtype=BF)
+    for rot, shape in ((three, (5, 3)), (one, (5,)), (one, (5, 1)), (tuple_of_one, (5,))):
+        pos = torch.zeros(shape, dtype=torch.int32)
+        assert rot.tables(pos) == "tables" and rot(x, pos) == "turned"
+    for rot, shape in ((three, (5,)), (three, (5, 2)), (three, (5, 4)), (one, (5, 3)), (tuple_of_one, (5, 2))):
+        pos = torch.zeros(shape, dtype=torch.int32)
+        with pytest.raises(ValueError, match="positions"):
+            rot.tables(pos)
+        with pytest.raises(ValueError, match="positions"):
+            rot(x, pos)
