@@ -47,6 +47,7 @@ struct DeviceInfo {
   int int4_pairs = 0;  // the same for the INT4 GEMM
   int mlp_pairs = 0;   // the same for the fused MLP's fc1
   int w8_pairs = 0;    // the same for the 8-bit GEMM
+  int w8_clusters[3] = {};  // co-resident clusters of 2, 4, 8 of the streaming 8-bit kernel, an SM to each CTA
   int gemm_pair_mode = -1;  // -1: by shape; SVDQ_GEMM_PAIR=0/1 forces single-CTA / CTA-pair tiles
   uint32_t* status = nullptr;
   float* xl1_scratch = nullptr;  // device address of g_xl1_scratch
@@ -209,14 +210,14 @@ svdq_status device_setup(DeviceInfo** out) {
     {
       // how many 2-CTA clusters of the pair GEMM can be resident at once (a
       // persistent grid larger than that would run its last clusters late)
-      auto pairs = [&](auto kern, int threads, size_t smem) {
+      auto clusters_of = [&](auto kern, int threads, size_t smem, int size, int most) {
         cudaLaunchConfig_t q = {};
-        q.gridDim = dim3(2 * (d.num_sms / 2), 1, 1);
+        q.gridDim = dim3(size * most, 1, 1);
         q.blockDim = dim3(threads, 1, 1);
         q.dynamicSmemBytes = smem;
         cudaLaunchAttribute a[1];
         a[0].id = cudaLaunchAttributeClusterDimension;
-        a[0].val.clusterDim.x = 2;
+        a[0].val.clusterDim.x = size;
         a[0].val.clusterDim.y = 1;
         a[0].val.clusterDim.z = 1;
         q.attrs = a;
@@ -224,14 +225,19 @@ svdq_status device_setup(DeviceInfo** out) {
         int clusters = 0;
         if (cudaOccupancyMaxActiveClusters(&clusters, kern, &q) != cudaSuccess || clusters <= 0) {
           (void)cudaGetLastError();
-          clusters = d.num_sms / 2;
+          clusters = most;
         }
-        return clusters < d.num_sms / 2 ? clusters : d.num_sms / 2;
+        return clusters < most ? clusters : most;
+      };
+      auto pairs = [&](auto kern, int threads, size_t smem) {
+        return clusters_of(kern, threads, smem, 2, d.num_sms / 2);
       };
       d.gemm_pairs = pairs(w4a4_nvfp4_gemm_kernel<true>, kGmThreads, GmCfg<true>::kSmemBytes);
       d.int4_pairs = pairs(w4a4_int4_gemm_kernel<true>, kI4Threads, kI4SmemBytes);
       d.mlp_pairs = pairs(w4a4_mlp_fc1_kernel, kMlThreads, kMlSmemBytes);
       d.w8_pairs = pairs(w8a8_gemm_kernel<false, false>, kW8Threads, kW8SmemBytes);
+      for (int i = 0; i < 3; ++i)
+        d.w8_clusters[i] = clusters_of(w8a8_stream_kernel<false, true>, kWsThreads, kWsWholeSm, 2 << i, d.num_sms / (2 << i));
       if (std::getenv("SVDQ_DEBUG") != nullptr)
         std::fprintf(stderr, "svdq: %d SMs, %d / %d co-resident NVFP4 / INT4 GEMM CTA pairs\n",
                      d.num_sms, d.gemm_pairs, d.int4_pairs);
@@ -1154,14 +1160,31 @@ svdq_status launch_w8a8_gemv(const DeviceInfo* d, bool gated, const W8Params& q,
 }
 
 // How the streaming kernel takes a product: token tiles of T, and a cluster of `splits` CTAs
-// per tile of 128 weight rows, the smallest power of two (at most 8, at most half the K
-// tiles) that gives four in five SMs a CTA (77 tokens, K = 3840: N = 3840 takes 14.7, 11.1, 9.2, 10.9 us
-// with 1, 2, 4, 8; N = 15360 17.7, 17.7, 23.9).
+// (at most 8, at most half the K tiles) per tile of 128 weight rows.
 struct StreamPlan {
   long long tiles;             // of weight rows
   int token_tiles, T, ktiles, splits;
-  bool full;                   // tiles enough without splitting
 };
+// More clusters than can run with an SM to each CTA (33 of four, 15 of eight: they leave some SMs
+// out): two CTAs to an SM. 64 x 5120 x 4736 in clusters of four, 37 of them: 16.8 us as two waves.
+bool stream_shares(const DeviceInfo* d, const StreamPlan& s, int splits) {
+  const int most = splits == 1 ? d->num_sms : d->w8_clusters[splits == 8 ? 2 : splits / 4];
+  return s.tiles * s.token_tiles > most;
+}
+// One token tile, in ns: the sum over a cluster and its set-up against the stages of K that it
+// saves, both growing with T; a stage's way in, longer in wider clusters, or all SMs' share of
+// the memory; CTAs that share an SM end one after the other. Fitted to 222 shapes (up to 104 row
+// tiles, K 512 to 15360, 4 to 128 tokens) timed with every count: the choice is 0.3 % slower than the
+// fastest on average, 9 % at worst. 64 tokens, (K, N): (1024, 5760) takes 5.0, 5.8, 6.5 us with
+// 1, 2, 4; (3840, 3840) 10.3, 9.3, 8.4, 9.5 with 1, 2, 4, 8; (12288, 1024) 28.4, 18.1, 11.4, 8.9.
+long long stream_cost(const DeviceInfo* d, const StreamPlan& s, int splits) {
+  long long stage = 280;
+  for (int i = splits; i > 1; i /= 2) stage += 40;
+  const long long own = (s.ktiles + splits - 1) / splits * stage, all = s.tiles * s.ktiles * 16 / 10;
+  long long cost = (own > all ? own : all) + (splits == 1 ? 2200 + 18ll * s.T : 4500 + 23ll * s.T);
+  if (splits > 1 && stream_shares(d, s, splits)) cost += 350 + 45ll * s.T;
+  return cost;
+}
 StreamPlan stream_plan(const DeviceInfo* d, bool gated, int M, int N, int K) {
   StreamPlan s;
   const int tile_n = gated ? 64 : 128;
@@ -1169,14 +1192,17 @@ StreamPlan stream_plan(const DeviceInfo* d, bool gated, int M, int N, int K) {
   s.token_tiles = (M + kWsMaxT - 1) / kWsMaxT;
   s.T = ((M + s.token_tiles - 1) / s.token_tiles + 15) / 16 * 16;
   s.ktiles = (K + kW8KStage - 1) / kW8KStage;
-  s.full = 5 * s.tiles * s.token_tiles >= 4ll * d->num_sms;
   s.splits = 1;
-  while (s.splits < 8 && 2 * s.splits <= s.ktiles && 5 * s.tiles * s.token_tiles * s.splits < 4ll * d->num_sms)
-    s.splits *= 2;
+  if (s.token_tiles == 1) {
+    for (int n = 2, i = 0; n <= 8 && 2 * n <= s.ktiles && s.tiles <= 2 * d->w8_clusters[i]; n *= 2, ++i)
+      if (stream_cost(d, s, n) < stream_cost(d, s, s.splits)) s.splits = n;
+  } else {  // where token tiles are chosen at all: the smallest that gives four in five SMs a CTA
+    while (s.splits < 8 && 2 * s.splits <= s.ktiles && 5 * s.tiles * s.token_tiles * s.splits < 4ll * d->num_sms)
+      s.splits *= 2;
+  }
   return s;
 }
 
-// More CTAs than SMs share them two by two.
 svdq_status launch_w8a8_stream(const DeviceInfo* d, bool gated, const W8Params& q, const StreamPlan& plan,
                                const void* a_codes, const void* w_codes, void* Y, int ldy, svdq_stream_t stream) {
   WsParams p;
@@ -1189,9 +1215,9 @@ svdq_status launch_w8a8_stream(const DeviceInfo* d, bool gated, const W8Params& 
   if (plan.tiles > INT32_MAX / 8 || plan.token_tiles > 65535) return SVDQ_ERR_UNSUPPORTED;
   const int tiles = static_cast<int>(plan.tiles);
   p.splits = splits;
-  p.shared = plan.tiles * plan.token_tiles * splits > d->num_sms;
+  p.shared = stream_shares(d, plan, splits);
   // two CTAs to an SM also for the widest clusters: few of eight whole SMs each find room at once
-  const size_t budget = p.shared || splits == 8 ? 113 * 1024 : 226 * 1024;
+  const size_t budget = p.shared || splits == 8 ? kWsHalfSm : kWsWholeSm;
   const int per_cta = (ktiles + splits - 1) / splits;
   int stages = kWsMaxStages;
   while (stages > 2 && (ws_smem_bytes(p.T, stages) > budget || stages > per_cta)) --stages;
@@ -1257,17 +1283,17 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   // One to sixteen tokens of a small weight: no set-up (one token: K = N = 1024 2.5 us against 3.7
   // streamed, K = N = 3840 5.9 against 7.1; sixteen: K = N = 1024 2.9 against 4.0). Where a warp would go
   // round more than once, or the SMs get more than two blocks each, the copies of the streaming
-  // kernel keep more bytes on their way (one token: K = 15360, N = 3840 15.8 against 13.1, K = 3840,
-  // N = 15360 15.7 against 12.9; sixteen: K = N = 3840 9.7 against 7.5).
+  // kernel keep more bytes on their way (one token: K = 15360, N = 3840 15.8 against 13.6, K = 3840,
+  // N = 15360 19.0 against 12.2; sixteen: K = N = 3840 10.9 against 7.4).
   if (M <= kWvMaxM && K <= (M <= 8 ? 4096 : 2048) && N / (gated ? 8 : 16) <= 2 * d->num_sms)
     return launch_w8a8_gemv(d, gated, p, a_codes, w_codes, Y, ldy, stream);
-  // Few tokens stream the weight (64 tokens, streamed / in CTA pairs: K = N = 1024 5.0 / 4.8 us,
-  // K = N = 3840 8.8 / 10.1, K = 1024, N = 15360 9.9 / 12.1). Above 64 only where the tiles
-  // suffice without sharing K, or K is long: the sum over a cluster grows with the tokens (128 tokens: K = N = 1024
-  // 6.5 / 5.2, K = 2048, N = 3840 9.1 / 8.4, K = N = 3840 10.8 / 10.6, K = 1024, N = 15360 12.7 / 12.9,
-  // K = 15360, N = 3840 18.2 / 26.4).
+  // Few tokens stream the weight (64 tokens, streamed / in CTA pairs: K = N = 1024 4.8 / 4.7 us,
+  // K = 1024, N = 15360 7.4 / 10.4). Above 64 only where the row tiles reach three in five SMs, or K
+  // is long: the epilogue of a tile grows with the tokens (128 tokens: K = N = 1024 6.1 / 4.6, K = 2048,
+  // N = 3840 8.0 / 7.3, K = 1024, N = 15360 10.2 / 11.1, K = 3840,
+  // N = 2560 9.0 / 9.1, N = 15360 17.1 / 20.9).
   const StreamPlan plan = stream_plan(d, gated, M, N, K);
-  if (M <= 64 || (M <= kWsMaxT && (plan.full || K >= 3500)))
+  if (M <= 64 || (M <= kWsMaxT && (5 * plan.tiles >= 3ll * d->num_sms || K >= 3500)))
     return launch_w8a8_stream(d, gated, p, plan, a_codes, w_codes, Y, ldy, stream);
   // The tile's width: the one whose waves of tiles over the CTA pairs take least, a stage
   // of K costing its operands' way in, 256 + bn rows per pair (at 256 columns that equals its

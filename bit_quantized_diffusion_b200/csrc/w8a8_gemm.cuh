@@ -114,6 +114,15 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t a, uint32_t b, uint32_t (&r
       : "r"(b));
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+
 template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kW8Threads, 1)
     w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -416,24 +425,29 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 }
 
 // w8a8_stream_kernel: up to 128 tokens (or tiles of as many, where a long K meets few
-// columns), where the product is bound by reading the weight once. The operands change sides: 128 weight rows are the MMA's M (tensor-memory
-// lanes), the tokens, rounded up to 16, its N, so a handful of tokens costs no padding
-// to 256 rows. One tile of 128 weight rows (gated: 64 gate rows and the 64 matching up
+// columns), where the product is bound by reading the weight once. The operands change sides: 128
+// weight rows are the MMA's M (tensor-memory lanes), the tokens, rounded up to 16, its N, so a
+// handful of tokens costs no padding to 256 rows. One tile of 128 weight rows (gated: 64 gate rows and the 64 matching up
 // rows) per cluster, whose CTAs split K and add their float32 partial sums through
 // distributed shared memory, in rank order: weights narrower than a row tile per SM
 // still keep every SM loading, without memory to add in and without atomics.
 // Bound by HBM: gated, 4 x 3840 x 10240, 78.8 MB: 15.0 us, 5.2 TB/s; 77 x 3840 x 15360 with GELU,
-// 61.7 MB: 15.5 us (launch, the first copies and the sum in shared memory are 5 us of it).
+// 61.7 MB: 14.9 us; 128 x 3840 x 15360 with a residual, 67.3 MB: 17.0 us. (Unsplit tiles too through
+// shared memory [T][128] and 8-byte stores by all warps: 15.0, 15.5 and 19.5 us.)
 //
 //   warp 0     TMA producer: W [2 x 64 rows x 128 B] and X [T x 128 B] per stage
 //   warp 1     tensor-memory owner and MMA issuer (one thread)
-//   warps 2-9  the residual's lines into L2; then accumulator -> shared memory [T][128],
-//              two warps per tensor-memory lane quadrant
-//   all warps  the sum over the cluster and the epilogue, four adjacent outputs per
+//   warps 2-9  the residual's lines into L2; then the accumulator, two warps per tensor-memory
+//              lane quadrant. One CTA per tile: straight to the outputs, a lane per weight row,
+//              whose scale, bias and residual it holds by then (gated, the gate's warps take half
+//              of the tokens and the up rows' the other half, and each hands the other's over
+//              through shared memory). A cluster: to shared memory [T][128]
+//   all warps  of a cluster: the sum over it and the epilogue, four adjacent outputs per
 //              thread and step, a thread's columns the same in every step
 constexpr int kWsThreads = 320;
 constexpr int kWsMaxT = 128;
 constexpr int kWsMaxStages = 12;
+constexpr size_t kWsWholeSm = 226 * 1024, kWsHalfSm = 113 * 1024;  // a CTA's shared memory, at most
 
 struct WsParams {
   int M, N, K;                 // N: output columns (F when gated)
@@ -555,9 +569,9 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // this CTA's share of the tile's outputs: items of four adjacent columns, e .. e1 in
+  // a CTA's share of its cluster's outputs: items of four adjacent columns, e .. e1 in
   // steps of the block, which keep a thread at the same columns; their scales and bias now
-  constexpr int kQuads = kCols / 4, kStep = kSplit ? 1 : (kGated ? 2 : 4);
+  constexpr int kQuads = kCols / 4;
   static_assert(kWsThreads % kQuads == 0, "a thread keeps its columns");
   const int items = rows * kQuads;
   const int e1 = (rank + 1) * items / splits;
@@ -565,24 +579,21 @@ __global__ void __launch_bounds__(kWsThreads, 2)
   const int c = 4 * (e % kQuads), n = n0 + c;
   float sw[kGated ? 8 : 4], bias[kGated ? 8 : 4];
 #pragma unroll
-  for (int q = 0; q < (kGated ? 8 : 4); ++q) {
+  for (int q = 0; kSplit && q < (kGated ? 8 : 4); ++q) {
     const int row = (q < 4 ? n : p.N + n) + (q & 3);
     sw[q] = n < p.N ? p.w_scale[row] : 0.0f;
     bias[q] = n < p.N && p.bias != nullptr ? __bfloat162float(p.bias[row]) : 0.0f;
   }
   // a step's residual, the first now, each other one a step ahead
-  float r[kStep][4];
+  float r[4];
   auto residual = [&](int from) {
-#pragma unroll
-    for (int j = 0; j < kStep; ++j)
-      if (p.residual != nullptr && n < p.N && from + j * kWsThreads < e1)
-        w8_load4(p.residual, static_cast<size_t>(m0 + (from + j * kWsThreads) / kQuads) * p.ldr + n, p.out_f32, r[j]);
+    if (p.residual != nullptr && n < p.N && from < e1)
+      w8_load4(p.residual, static_cast<size_t>(m0 + from / kQuads) * p.ldr + n, p.out_f32, r);
   };
-  residual(e);
+  if (kSplit) residual(e);
   // the cluster's four sums of row m from accumulator column col, in rank order
   auto sum4 = [&](int m, int col) {
     const uint32_t at = sbase + (m * 128 + col) * 4;
-    if (!kSplit) return lds_f4(at);
     float4 v = lds_cluster_f4(map_peer_smem(at, 0));
 #pragma unroll 4
     for (int r = 1; r < splits; ++r) {
@@ -626,7 +637,8 @@ __global__ void __launch_bounds__(kWsThreads, 2)
     const int quad = warp & 3;
     for (int i = threadIdx.x - 64; i < rows; i += kWsThreads - 64) sa_s[i] = p.a_scale[m0 + i];
     if (p.residual != nullptr) {
-      // the rest of the residual: read at the very end, from memory it would add a latency per step
+      // the residual in whole lines: what is read at the end would add a latency per step, and a lane's
+      // two bytes of many rows, unsplit, reach memory slower (100 x 512 x 15360: 8.6 us, without 9.4)
       const int esz = p.out_f32 ? 4 : 2, lines = kCols * esz / 128;
       for (int i = threadIdx.x - 64; i < rows * lines; i += kWsThreads - 64) {
         const int col = n0 + (i % lines) * (128 / esz);
@@ -635,69 +647,165 @@ __global__ void __launch_bounds__(kWsThreads, 2)
                                                         (static_cast<size_t>(m0 + i / lines) * p.ldr + col) * esz));
       }
     }
-    // the stages' memory is free once the last MMA is done
-    bool ok = mbar_wait(bar_acc, 0, p.status);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      float* part = reinterpret_cast<float*>(smem);  // [T][128]
-      for (int c = (warp - 2) / 4 * 32; c < T; c += 64) {
-        uint32_t acc[32];
-        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, acc);
-        tmem_ld_wait();
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int half = (warp - 2) / 4;
+    if constexpr (kSplit) {
+      // the stages' memory is free once the last MMA is done
+      bool ok = mbar_wait(bar_acc, 0, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        float* part = reinterpret_cast<float*>(smem);  // [T][128]
+        for (int c = half * 32; c < T; c += 64) {
+          uint32_t acc[32];
+          tmem_ld32(t_row + c, acc);
+          tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 32; ++q)
-          if (c + q < T) part[(c + q) * 128 + quad * 32 + lane] = __uint_as_float(acc[q]);
+          for (int q = 0; q < 32; ++q)
+            if (c + q < T) part[(c + q) * 128 + quad * 32 + lane] = __uint_as_float(acc[q]);
+        }
+        tc_fence_before();
+      }
+    } else {
+      // every other 16 tokens of the quadrant's rows; gated, eight of each 16 per warp
+      constexpr int kKeep = kGated ? 8 : 16;
+      const bool up = kGated && quad >= 2;
+      const int col = (kGated ? quad & 1 : quad) * 32 + lane, n = n0 + col, first = up ? 8 : 0;
+      const bool in = n < p.N;
+      const float sw = in ? p.w_scale[n] : 0.0f, usw = kGated && in ? p.w_scale[p.N + n] : 0.0f;
+      const float bias = in && p.bias != nullptr ? __bfloat162float(p.bias[n]) : 0.0f;
+      const float ubias = kGated && in && p.bias != nullptr ? __bfloat162float(p.bias[p.N + n]) : 0.0f;
+      // the residual of the warp's 16 tokens k: all of it now in bf16, two values to a register; in
+      // float32 two k ahead
+      uint32_t res[kGated ? 1 : 32];
+      const bool add = !kGated && p.residual != nullptr && in;
+      auto read_residual = [&](int k) {
+        const int from = half * 16 + 32 * k;
+        if (add && from < rows) {
+          // (behind the last row: that one again, so that no branch parts the loads)
+          auto at = [&](int q) { return static_cast<size_t>(min(from + q, rows - 1)) * p.ldr + n; };
+          if (p.out_f32) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              res[k % 2 * 16 + q] = __float_as_uint(static_cast<const float*>(p.residual)[at(q)]);
+          } else {
+            uint32_t v[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = static_cast<const uint16_t*>(p.residual)[at(q)];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) res[k * 8 + q] = v[2 * q] | v[2 * q + 1] << 16;
+          }
+        }
+      };
+      if constexpr (!kGated) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < 2 || !p.out_f32) read_residual(k);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the tokens' scales
+      bool ok = mbar_wait(bar_acc, 0, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      if (p.shared) grid_dep_launch();
+      float* other = reinterpret_cast<float*>(smem) + col;  // [T][64], in the stages' memory, free now
+      uint32_t acc[16];
+      if (kGated) {
+        for (int c = half * 16; ok && c < T; c += 32) {
+          tmem_ld16(t_row + c, acc);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) other[(c + 8 - first + q) * 64] = __uint_as_float(up ? acc[q] : acc[8 + q]);
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // (also after a wait has run out)
+      }
+#pragma unroll
+      for (int k = 0; k < kWsMaxT / 32; ++k) {
+        const int c = half * 16 + 32 * k;
+        if (!ok || c >= T) break;
+        tmem_ld16(t_row + c, acc);
+        tmem_ld_wait();
+        float2 y[kKeep / 2];  // of tokens 2 q, 2 q + 1 (behind the last row: the scale of none, not stored)
+#pragma unroll
+        for (int q = 0; q < kKeep / 2; ++q) {
+          const int m = c + first + 2 * q;
+          const float2 sa = *reinterpret_cast<const float2*>(sa_s + m);
+          const float2 v = __fmul2_rn(up ? make_float2(__uint_as_float(acc[(2 * q + 8) % 16]), __uint_as_float(acc[(2 * q + 9) % 16]))
+                                         : make_float2(__uint_as_float(acc[2 * q]), __uint_as_float(acc[2 * q + 1])), sa);
+          if constexpr (kGated) {
+            const float2 o = __fmul2_rn(make_float2(other[m * 64], other[(m + 1) * 64]), sa);
+            const float2 gate = __ffma2_rn(up ? o : v, make_float2(sw, sw), make_float2(bias, bias));
+            const float2 through = __ffma2_rn(up ? v : o, make_float2(usw, usw), make_float2(ubias, ubias));
+            y[q] = __fmul2_rn(make_float2(w8_act(gate.x, p.act), w8_act(gate.y, p.act)), through);
+          } else {
+            const float2 z = __ffma2_rn(v, make_float2(sw, sw), make_float2(bias, bias));
+            y[q] = make_float2(w8_act(z.x, p.act), w8_act(z.y, p.act));
+          }
+        }
+        if constexpr (!kGated) {
+          if (add) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint32_t two = res[k * 8 + q], a = res[k % 2 * 16 + 2 * q], b = res[k % 2 * 16 + 2 * q + 1];
+              y[q] = __fadd2_rn(y[q], make_float2(__uint_as_float(p.out_f32 ? a : two << 16),
+                                                  __uint_as_float(p.out_f32 ? b : two & 0xFFFF0000u)));
+            }
+          }
+          if (k < 2 && p.out_f32) read_residual(k + 2);
+        }
+        if (p.out_f32) {
+          float* at = static_cast<float*>(p.Y) + static_cast<size_t>(c + first) * p.ldy + n;
+#pragma unroll
+          for (int q = 0; q < kKeep; ++q) {
+            if (in && c + first + q < rows) *at = q % 2 ? y[q / 2].y : y[q / 2].x;
+            at += p.ldy;
+          }
+        } else {
+          // neighbouring lanes trade a token each: a lane stores two columns of every other token
+          const bool odd = lane & 1;
+          __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.Y) + static_cast<size_t>(c + first + odd) * p.ldy + (n - odd);
+#pragma unroll
+          for (int q = 0; q < kKeep / 2; ++q) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? y[q].x : y[q].y, 1);
+            const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(got, y[q].y) : __floats2bfloat162_rn(y[q].x, got);
+            if (in && c + first + odd + 2 * q < rows) *reinterpret_cast<__nv_bfloat162*>(at) = two;
+            at += 2 * p.ldy;
+          }
+        }
       }
       tc_fence_before();
     }
   }
   if (kSplit) cluster_sync_converged(); else cta_sync_converged();
-  if (p.shared) grid_dep_launch();
+  if (kSplit && p.shared) grid_dep_launch();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tb);
   }
-  if (n < p.N) {
-    for (; e < e1; e += kStep * kWsThreads) {
-      float y[kStep][4];
-      float4 v4[kStep], w4[kStep];
+  if (kSplit && n < p.N) {
+    for (; e < e1; e += kWsThreads) {
+      const int m = e / kQuads;
+      const float sa = sa_s[m];
+      const float4 v = sum4(m, c);
+      float y[4];
+      y[0] = fmaf(v.x * sa, sw[0], bias[0]);
+      y[1] = fmaf(v.y * sa, sw[1], bias[1]);
+      y[2] = fmaf(v.z * sa, sw[2], bias[2]);
+      y[3] = fmaf(v.w * sa, sw[3], bias[3]);
 #pragma unroll
-      for (int j = 0; j < kStep; ++j)
-        if (e + j * kWsThreads < e1) {
-          v4[j] = sum4((e + j * kWsThreads) / kQuads, c);
-          if (kGated) w4[j] = sum4((e + j * kWsThreads) / kQuads, 64 + c);
-        }
-#pragma unroll
-      for (int j = 0; j < kStep; ++j) {
-        const int m = (e + j * kWsThreads) / kQuads;
-        if (e + j * kWsThreads < e1) {
-          const float sa = sa_s[m];
-          const float4 v = v4[j];
-          y[j][0] = fmaf(v.x * sa, sw[0], bias[0]);
-          y[j][1] = fmaf(v.y * sa, sw[1], bias[1]);
-          y[j][2] = fmaf(v.z * sa, sw[2], bias[2]);
-          y[j][3] = fmaf(v.w * sa, sw[3], bias[3]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) y[j][q] = w8_act(y[j][q], p.act);
-          if (kGated) {
-            const float4 w = w4[j];
-            y[j][0] *= fmaf(w.x * sa, sw[4], bias[4]);
-            y[j][1] *= fmaf(w.y * sa, sw[5], bias[5]);
-            y[j][2] *= fmaf(w.z * sa, sw[6], bias[6]);
-            y[j][3] *= fmaf(w.w * sa, sw[7], bias[7]);
-          }
-          if (p.residual != nullptr) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) y[j][q] += r[j][q];
-          }
-        }
+      for (int q = 0; q < 4; ++q) y[q] = w8_act(y[q], p.act);
+      if (kGated) {
+        const float4 w = sum4(m, 64 + c);
+        y[0] *= fmaf(w.x * sa, sw[4], bias[4]);
+        y[1] *= fmaf(w.y * sa, sw[5], bias[5]);
+        y[2] *= fmaf(w.z * sa, sw[6], bias[6]);
+        y[3] *= fmaf(w.w * sa, sw[7], bias[7]);
       }
-      residual(e + kStep * kWsThreads);
+      if (p.residual != nullptr) {
 #pragma unroll
-      for (int j = 0; j < kStep; ++j)
-        if (e + j * kWsThreads < e1)
-          w8_store4(p.Y, static_cast<size_t>(m0 + (e + j * kWsThreads) / kQuads) * p.ldy + n, p.out_f32, y[j]);
+        for (int q = 0; q < 4; ++q) y[q] += r[q];
+      }
+      residual(e + kWsThreads);
+      w8_store4(p.Y, static_cast<size_t>(m0 + m) * p.ldy + n, p.out_f32, y);
     }
   }
   // peers read this CTA's sums until here

@@ -234,6 +234,17 @@ def test_gated_linear(bq, M, F, K, bias, act, dtype):
     assert bq.svdq_check_device_status() == 0
 
 
+@TYPES
+@pytest.mark.parametrize("M", [17, 33, 47, 64, 77, 97, 128])
+def test_few_tokens_of_a_wide_weight(bq, M, dtype):
+    """A weight with row tiles enough for the GPU, each summed by one block: token counts about the
+    epilogue's groups of 16, columns that end inside a tile, with and without a residual."""
+    K = 272 if M % 2 else 1296
+    for act, residual in (("gelu", False), (None, True)):
+        test_linear(bq, M, 15136, K, M % 4 == 1, act, residual, dtype)
+    test_gated_linear(bq, M, 7600, K, M % 4 == 1, "silu", dtype)
+
+
 @pytest.mark.parametrize("M", [3, 20, 150, 300])
 def test_a_row_that_is_not_finite_touches_no_other(bq, M):
     N = K = 160
