@@ -164,7 +164,8 @@ def act_bound(z, ez, kind):
 
 
 CASES = [  # M, N, K, bias, act, residual: every kernel (few tokens of a small weight, of a large one with and
-    # without K shared by a cluster, CTA pairs of several widths), each at ragged sizes
+    # without K shared by a cluster, CTA pairs with a tile of 64 columns each), each at ragged sizes; wider
+    # tiles, and several to a pair, are in test_gpu_w8a8_tiles.py
     (1, 4752, 272, True, None, True), (3, 272, 4112, True, "silu", True), (8, 4736, 4096, True, None, False),
     (9, 160, 2048, False, None, True), (13, 15360, 144, True, "gelu", True), (16, 80, 2064, True, None, True),
     (340, 64, 12512, True, "gelu", True), (1000, 48, 4112, True, None, True), (130, 272, 4096, False, "silu", True),
