@@ -358,6 +358,34 @@ def test_gated_block_together(bq, M):
     assert bq.svdq_check_device_status() == 0
 
 
+@pytest.mark.parametrize("M", [1, 50, 300])
+def test_gated_block_without_a_residual(bq, M):
+    """The block on x alone, against its parts in float64 through the kernels' own codes: h is x
+    itself, and the projection is added to it, into a new tensor and in place."""
+    from bit_quantized_diffusion_b200.layers import W8A8GatedMlp
+    K, F = 512, 1040
+    gate, up = draw(1, F, K, dtype=BF, std=0.04), draw(2, F, K, dtype=BF, std=0.04)
+    down, norm = draw(3, K, F, dtype=BF, std=0.03), (1 + draw(4, K, std=0.1)).to(BF)
+    x = draw(5, M, K, dtype=BF, std=2.0)
+    block = W8A8GatedMlp.from_linears(gate, up, down, norm, max_tokens=M)
+    kept = x.clone()
+    y = block(x)
+    assert y is not x and torch.equal(x, kept)
+    h, n, rel = norm_bounds(x, norm, None, 1e-6, K)
+    check_norm(block.codes, block.scale[0], n, rel)
+    z, ez = product_bound(block.codes, block.scale[0], block.up["codes"], block.up["scale"], None, K)
+    g, eg = act_bound(z[:, :F], ez[:, :F], "silu")
+    hidden, e = g * z[:, F:], np.abs(g) * ez[:, F:] + np.abs(z[:, F:]) * eg
+    assert np.all(np.abs(f64(block.hidden) - hidden) <= 1.01 * e + (2.0 ** -8 + 2 * U) * (np.abs(hidden) + e))
+    codes, scale = O.quantize_rows(f64(block.hidden))
+    assert np.array_equal(f64(block.hidden_codes), codes) and np.array_equal(f64(block.scale[1]), scale)
+    z, ez = product_bound(block.hidden_codes, block.scale[1], block.down["codes"], block.down["scale"], None, F)
+    want = z + h
+    assert np.all(np.abs(f64(y) - want) <= 1.01 * ez + (2.0 ** -8 + 2 * U) * (np.abs(want) + ez))
+    assert block(x, y=x) is x and torch.equal(x, y)
+    assert bq.svdq_check_device_status() == 0
+
+
 @pytest.mark.parametrize("M", [1, 8, 40, 100, 300, 1500])
 def test_chain_on_one_buffer(bq, M):
     """Layer after layer on one residual stream and one set of workspaces, each call reading what
