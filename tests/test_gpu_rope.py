@@ -251,3 +251,45 @@ def test_frequencies_that_are_not_finite(bq):
                              bq.svdq_rope_table(pos, odd, angle_major=angle_major)):
             want, got = (t.t() if angle_major else t for t in (want, got))
             assert got[:, lost].isnan().all() and torch.equal(got[:, ~lost], want[:, ~lost])
+
+
+@pytest.mark.parametrize("M,P", [(9, 1), (700, 4), (700, 6)])
+@pytest.mark.parametrize("angle_major", [False, True], ids=["rows", "angle-major"])
+def test_positions_past_32_bits(bq, M, P, angle_major):
+    """int64 positions up to 2^40 either way, whose upper half counts. The fraction of a turn carries
+    freq's 53 bits and is cut at 2^-64: an angle is off by 2^-52 of itself and 2^-64 turns (2^-61
+    radians) a position."""
+    freq = torch.full((P,), math.pi / 2, dtype=torch.float64)
+    freq[P // 2:] = torch.linspace(1.0, 1e-9, P - P // 2, dtype=torch.float64)
+    far = torch.tensor([2 ** 33, -2 ** 33, 2 ** 33 + 1, 2 ** 40, 2 ** 40 + 3, -2 ** 40 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 2])
+    g = torch.Generator().manual_seed(M)
+    pos = torch.cat([far, torch.randint(-2 ** 40, 2 ** 40, (M - 9,), generator=g)]).cuda()
+    cos, sin = bq.svdq_rope_table(pos, freq.cuda(), angle_major=angle_major)
+    cos, sin = (f64(t.t() if angle_major else t) for t in (cos, sin))
+    p = pos.cpu().numpy()[:, None]
+    angle = p * freq.numpy()                                   # rounded once: 2^-53 of itself
+    e = 2.0 ** -22 + np.abs(angle) * (2.0 ** -52 + 2.0 ** -53) + np.abs(p) * 2.0 ** -61
+    assert np.all(np.abs(cos - np.cos(angle)) <= e) and np.all(np.abs(sin - np.sin(angle)) <= e)
+    # a whole number of quarter turns, whatever the bits of pi that float64 lacks add up to
+    if P > 1:
+        quarter = p[:, 0] % 4
+        q = 2.0 ** -22 + np.abs(p[:, 0]) * 2.0 ** -50
+        assert np.all(np.abs(cos[:, 0] - np.array([1, 0, -1, 0])[quarter]) <= q)
+        assert np.all(np.abs(sin[:, 0] - np.array([0, 1, 0, -1])[quarter]) <= q)
+
+
+@pytest.mark.parametrize("dtype,D,pairs,pad", [(F32, 2064, 512, 0), (F32, 2064, 500, 2), (BF, 1040, 512, 2), (BF, 4112, 512, 0),
+                                               (BF, 1300, 321, 2)])
+@pytest.mark.parametrize("interleaved", [True, False], ids=["adjacent", "halves"])
+def test_heads_of_more_vectors_than_a_block(bq, dtype, D, pairs, pad, interleaved):
+    """Heads that a block's 256 threads walk over more than once, with copied columns behind the
+    pairs: packed, in place, and beside heads that stay."""
+    freq = torch.logspace(0, -3, pairs, dtype=torch.float64).cuda()
+    pos = positions(D, 5, 1, 10000)
+    for H in (1, 9):
+        base = torch.randn(5, H + 1, D + pad, generator=torch.Generator().manual_seed(H)).to(dtype).cuda()
+        x, last = base[:, :H, :D], base[:, H].clone()
+        y = bq.svdq_rope(x, pos, freq, scale=1.25, interleaved=interleaved)
+        check(y, x, pos, freq, None, 1.25, interleaved)
+        assert bq.svdq_rope(x, pos, freq, scale=1.25, interleaved=interleaved, Y=x) is x
+        assert torch.equal(x, y) and torch.equal(base[:, H], last)
