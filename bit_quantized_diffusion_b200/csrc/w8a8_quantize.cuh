@@ -13,7 +13,8 @@
 // instructions (4608 of 3840, 53 MB: 13.9 us). The
 // floor 2^-100 keeps 448 / t finite, so an all-zero row has scale 2^-100 / 448 and
 // codes 0 and no case of its own. The maximum is taken on the bits of |y|, where NaN
-// is above infinity is above every number: a row that holds NaN has scale NaN.
+// is above infinity is above every number: a row that holds NaN has scale NaN. Rows whose squares leave
+// float32's range go through the reductions a second time, scaled by a power of two.
 #pragma once
 
 #include "sm100.cuh"
@@ -85,34 +86,51 @@ __device__ __forceinline__ uint2 e4m3x8(const float2 (&v)[4]) {
   return make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16));
 }
 
-// One vector of the row on its way into registers: the residual's sum and its copy out,
-// the weight (as float32, or null: from memory), and this thread's part of both reductions.
+// h = X + residual of one vector.
 template <int kRow, bool kF32>
-__device__ __forceinline__ void w8_take(const W8QuantParams& p, size_t row, int v, const W8Vec<kF32>& xv,
-                                        const W8Vec<kF32>& rv, const float2* wv, float2 (&h)[4], float2& ss,
-                                        float& top) {
+__device__ __forceinline__ void w8_sum(const W8Vec<kF32>& xv, const W8Vec<kF32>& rv, float2 (&h)[4]) {
   w8_floats<kF32>(xv, h);
-  if (kRow != kW8Plain) {
-    if (kRow == kW8ResidualNorm) {
-      float2 r[4];
-      w8_floats<kF32>(rv, r);
+  if (kRow == kW8ResidualNorm) {
+    float2 r[4];
+    w8_floats<kF32>(rv, r);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = __fadd2_rn(h[j], r[j]);
-      const size_t at = row * p.ldo + static_cast<size_t>(v) * 8;
-      if constexpr (kF32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.residual_out) + at);
-        o[0] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-        o[1] = make_float4(h[2].x, h[2].y, h[3].x, h[3].y);
-      } else {
-        uint32_t w[4];
+    for (int j = 0; j < 4; ++j) h[j] = __fadd2_rn(h[j], r[j]);
+  }
+}
+
+// h in X's type, and its way out
+template <bool kF32>
+__device__ __forceinline__ W8Vec<kF32> w8_round(const float2 (&h)[4]) {
+  W8Vec<kF32> o;
+  if constexpr (kF32) {
+    o.v[0] = make_uint4(__float_as_uint(h[0].x), __float_as_uint(h[0].y), __float_as_uint(h[1].x), __float_as_uint(h[1].y));
+    o.v[1] = make_uint4(__float_as_uint(h[2].x), __float_as_uint(h[2].y), __float_as_uint(h[3].x), __float_as_uint(h[3].y));
+  } else {
+    uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 b = __float22bfloat162_rn(h[j]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual_out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 b = __float22bfloat162_rn(h[j]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
+    o.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return o;
+}
+template <bool kF32>
+__device__ __forceinline__ void w8_sum_out(const W8QuantParams& p, size_t row, int v, const W8Vec<kF32>& o) {
+  const size_t at = row * p.ldo + static_cast<size_t>(v) * 8;
+  uint4* to = kF32 ? reinterpret_cast<uint4*>(static_cast<float*>(p.residual_out) + at)
+                   : reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual_out) + at);
+#pragma unroll
+  for (int i = 0; i < (kF32 ? 2 : 1); ++i) to[i] = o.v[i];
+}
+
+// This thread's part of both reductions: the squares of h, and the maximum of h times its weight
+// (as float32, or null: from memory), which h leaves as.
+template <bool kNorm>
+__device__ __forceinline__ void w8_measure(const W8QuantParams& p, int v, const float2* wv, float2 (&h)[4], float2& ss,
+                                           float& top) {
+  if (kNorm) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) ss = __ffma2_rn(h[j], h[j], ss);
     if (p.weight != nullptr) {
@@ -165,29 +183,32 @@ __device__ __forceinline__ bool w8_reduce(float2 ss2, float top1, float& ss, flo
   return ok;
 }
 
-// The row's scale, and what turns its values into codes: one factor, or, where that would
-// leave float32's range (an all but empty row), rs and then inv.
+// The row's scale (or the mark of a row that comes once more: no scale is negative), and what turns its
+// values into codes: one factor, or, where that would leave float32's range (an all but empty row), rs
+// and then inv.
+constexpr float kW8Again = -1.0f;
 struct W8Factors {
   float one, rs, inv;
 };
 template <bool kNorm>
-__device__ __forceinline__ W8Factors w8_scale(const W8QuantParams& p, size_t row, float ss, float top) {
+__device__ __forceinline__ W8Factors w8_scale(const W8QuantParams& p, size_t row, float ss, float top, float eps,
+                                              bool again = false) {
   W8Factors f;
   float t = top;
   f.rs = 1.0f;
   if (kNorm) {
-    f.rs = rsqrtf(fmaf(ss, p.inv_k, p.eps));
+    f.rs = rsqrtf(fmaf(ss, p.inv_k, eps));
     t *= f.rs;
   }
   if (t < 7.888609052210118e-31f) t = 7.888609052210118e-31f;  // 2^-100; NaN stays
   f.inv = __fdiv_rn(448.0f, t);
   f.one = f.rs * f.inv;
-  if (threadIdx.x == 0) p.scale[row] = __fdiv_rn(t, 448.0f);
+  if (threadIdx.x == 0) p.scale[row] = again ? kW8Again : __fdiv_rn(t, 448.0f);
   return f;
 }
 
 template <bool kNorm, int kVecs>
-__device__ __forceinline__ void w8_give(const W8QuantParams& p, size_t row, float2 (&h)[kVecs][4], const W8Factors& f) {
+__device__ __forceinline__ void w8_give(const W8QuantParams& p, size_t row, float2 (&h)[kVecs][4], const W8Factors& f, int first) {
   float mul = f.one;
   if (kNorm && !(f.one < 1e37f)) {
 #pragma unroll
@@ -196,15 +217,74 @@ __device__ __forceinline__ void w8_give(const W8QuantParams& p, size_t row, floa
       for (int j = 0; j < 4; ++j) h[i][j] = __fmul2_rn(h[i][j], make_float2(f.rs, f.rs));
     mul = f.inv;
   }
-  uint2* out = reinterpret_cast<uint2*>(p.codes + row * static_cast<size_t>(p.K)) + threadIdx.x;
+  uint2* out = reinterpret_cast<uint2*>(p.codes + row * static_cast<size_t>(p.K)) + first;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
-    if (static_cast<int>(threadIdx.x + i * blockDim.x) < p.K / 8) {
+    if (static_cast<int>(first + i * blockDim.x) < p.K / 8) {
       float2 q[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) q[j] = __fmul2_rn(h[i][j], make_float2(mul, mul));
       out[i * blockDim.x] = e4m3x8(q);
     }
+}
+
+// Squares leave float32's range long before the values do. Where their sum overflowed, or is so small (and
+// eps too) that squares were lost, the row goes through both reductions once more, times this power of
+// two, and eps times its square: y is the same. 1 where neither holds; the same in every thread of
+// the block. Up to K = 2^15 values the second sum keeps its range: below 2^15 (2^128 2^-100)^2 = 2^71, and
+// below 2^15 2^-90 2^200 = 2^125. (A row that holds infinity comes here too; its scale stays not finite.)
+__device__ __forceinline__ float w8_rescale(const W8QuantParams& p, float ss) {
+  if (ss > 3.402823466e38f) return 7.888609052210118e-31f;                                   // 2^-100
+  return fmaf(ss, p.inv_k, p.eps) < 8.077935669463161e-28f ? 1.2676506002282294e30f : 1.0f;  // 2^-90, 2^100
+}
+
+// Such a row from its beginning, out of memory: x and r (float32 sums: the sum, and no r), with its
+// 16-bit sum's copy out. Out of line, its parameters by value, and called where nothing of the common
+// way is live any more: inside the ring's loop, or with the address of the kernel's parameters, it cost
+// every row 7 to 13 %. Each thread touches the vectors that it had before.
+template <int kRow, bool kF32>
+__device__ __noinline__ void w8_row_again(const W8QuantParams p, size_t row, const void* x, const void* r,
+                                          float2 (*part)[32]) {
+  float2 h[1][4], ss2;
+  float ss, top, f = 1.0f;
+  auto sum = [&](int v) {
+    const W8Vec<kF32> xv = w8_load<kF32>(x, static_cast<size_t>(v) * 8);
+    w8_sum<kRow, kF32>(xv, kRow == kW8ResidualNorm ? w8_load<kF32>(r, static_cast<size_t>(v) * 8) : xv, h[0]);
+  };
+  auto measure = [&](int v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[0][j] = __fmul2_rn(h[0][j], make_float2(f, f));
+    w8_measure<true>(p, v, nullptr, h[0], ss2, top);
+  };
+  for (int pass = 0; pass == 0 || (pass == 1 && f != 1.0f); ++pass) {
+    ss2 = make_float2(0.0f, 0.0f);
+    top = 0.0f;
+#pragma unroll 1
+    for (int v = threadIdx.x; v < p.K / 8; v += blockDim.x) {
+      sum(v);
+      measure(v);
+    }
+    w8_reduce<true>(ss2, top, ss, top, true, part[pass]);
+    if (pass == 0) f = w8_rescale(p, ss);
+  }
+  const W8Factors g = w8_scale<true>(p, row, ss, top, p.eps * f * f);
+#pragma unroll 1
+  for (int v = threadIdx.x; v < p.K / 8; v += blockDim.x) {
+    sum(v);
+    if (kRow == kW8ResidualNorm) w8_sum_out<kF32>(p, row, v, w8_round<kF32>(h[0]));
+    measure(v);
+    w8_give<true, 1>(p, row, h, g, v);
+  }
+  __syncthreads();  // `part` is free
+}
+template <int kRow, bool kF32>
+__device__ __forceinline__ void w8_again(const W8QuantParams& p, size_t row, float2 (*part)[32]) {
+  constexpr size_t esz = kF32 ? 4 : 2;
+  if constexpr (kRow == kW8ResidualNorm && kF32)
+    w8_row_again<kW8Norm, kF32>(p, row, static_cast<const char*>(p.residual_out) + row * p.ldo * esz, nullptr, part);
+  else
+    w8_row_again<kRow, kF32>(p, row, static_cast<const char*>(p.X) + row * p.ldx * esz,
+                             kRow == kW8ResidualNorm ? static_cast<const char*>(p.residual) + row * p.ldr * esz : nullptr, part);
 }
 
 // One block per row; thread i holds the row's 8-value vectors i, i + blockDim.x, ...
@@ -213,10 +293,10 @@ template <int kRow, bool kF32>
 __global__ void __launch_bounds__(1024) w8a8_quantize_kernel(const W8QuantParams p) {
   constexpr bool kNorm = kRow != kW8Plain;
   constexpr int kVecs = 4;
-  __shared__ __align__(16) float2 part[32];
+  __shared__ __align__(16) float2 part[kNorm ? 2 : 1][32];
   const size_t row = blockIdx.x;
   const int nvec = p.K / 8, T = blockDim.x, tid = threadIdx.x;
-  if (tid < 32 && tid >= T / 32) part[tid] = make_float2(0.0f, 0.0f);
+  if (tid < 32 && tid >= T / 32) part[0][tid] = part[kNorm][tid] = make_float2(0.0f, 0.0f);
   grid_dep_wait();
   grid_dep_launch();
   float2 h[kVecs][4], ss2 = make_float2(0.0f, 0.0f);
@@ -230,12 +310,32 @@ __global__ void __launch_bounds__(1024) w8a8_quantize_kernel(const W8QuantParams
       if (kRow == kW8ResidualNorm) rv[i] = w8_load<kF32>(p.residual, row * p.ldr + static_cast<size_t>(v) * 8);
     }
   }
+  // A 16-bit sum leaves behind the reductions: it may go where the residual or X is, which a row that
+  // goes through them again still has to read. (A float32 one goes at once and is read again itself.)
+  constexpr bool kKeep = kRow == kW8ResidualNorm && !kF32;
+  W8Vec<kF32> sum[kKeep ? kVecs : 1];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
-    if (tid + i * T < nvec) w8_take<kRow, kF32>(p, row, tid + i * T, xv[i], rv[i], nullptr, h[i], ss2, top);
-  w8_reduce<kNorm>(ss2, top, ss, top, true, part);
-  const W8Factors f = w8_scale<kNorm>(p, row, ss, top);
-  w8_give<kNorm, kVecs>(p, row, h, f);
+    if (tid + i * T < nvec) {
+      w8_sum<kRow, kF32>(xv[i], rv[i], h[i]);
+      if constexpr (kKeep) sum[i] = w8_round<kF32>(h[i]);
+      else if (kRow == kW8ResidualNorm) w8_sum_out<kF32>(p, row, tid + i * T, w8_round<kF32>(h[i]));
+      w8_measure<kNorm>(p, tid + i * T, nullptr, h[i], ss2, top);
+    }
+  w8_reduce<kNorm>(ss2, top, ss, top, true, part[0]);
+  if constexpr (kNorm) {
+    if (w8_rescale(p, ss) != 1.0f) {
+      __syncthreads();  // `part` has been read
+      w8_again<kRow, kF32>(p, row, part);
+      return;
+    }
+  }
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (tid + i * T < nvec) w8_sum_out<kF32>(p, row, tid + i * T, sum[i]);
+  }
+  w8_give<kNorm, kVecs>(p, row, h, w8_scale<kNorm>(p, row, ss, top, p.eps), tid);
 }
 
 // Many rows: persistent blocks, each with a ring of rows (X, then the residual) that bulk
@@ -293,6 +393,7 @@ __global__ void __launch_bounds__(1024) w8a8_quantize_ring_kernel(const W8QuantP
       for (int j = 0; j < 4; ++j) weight[(tid + i * T) * 4 + j] = g[j];
     }
   int s = 0, phase = 0, odd = 0;
+  bool again = false;  // a row's squares left float32's range
   for (size_t row = blockIdx.x; row < q.M; row += gridDim.x) {
     bool ok = mbar_wait(bars + 8 * s, phase, q.status);
     float2 h[kVecs][4], ss2 = make_float2(0.0f, 0.0f);
@@ -305,7 +406,9 @@ __global__ void __launch_bounds__(1024) w8a8_quantize_ring_kernel(const W8QuantP
         const W8Vec<kF32> xv = w8_load<kF32>(st, static_cast<size_t>(v) * 8);
         W8Vec<kF32> rv = xv;
         if (has_r) rv = w8_load<kF32>(st + x_bytes, static_cast<size_t>(v) * 8);
-        w8_take<kRow, kF32>(p, row, v, xv, rv, weight + v * 4, h[i], ss2, top);
+        w8_sum<kRow, kF32>(xv, rv, h[i]);
+        if (has_r) w8_sum_out<kF32>(p, row, v, w8_round<kF32>(h[i]));
+        w8_measure<kNorm>(p, v, weight + v * 4, h[i], ss2, top);
       }
     }
     // the exchange's barrier also says that the stage has been read
@@ -317,12 +420,30 @@ __global__ void __launch_bounds__(1024) w8a8_quantize_ring_kernel(const W8QuantP
       }
       break;
     }
+    const bool rare = kNorm && w8_rescale(p, ss) != 1.0f;
+    again |= rare;
+    if constexpr (has_r && !kF32) {
+      // a sum in place is taken back: the row is read once more
+      if (rare && (p.residual_out == p.X || p.residual_out == p.residual)) {
+        const uint8_t* was = p.residual_out == p.X ? st : st + x_bytes;
+#pragma unroll 1
+        for (int v = tid; v < nvec; v += T)
+          w8_sum_out<kF32>(p, row, v, w8_load<kF32>(was, static_cast<size_t>(v) * 8));
+        __syncthreads();
+      }
+    }
     const size_t next = row + static_cast<size_t>(NS) * gridDim.x;
     if (tid == 0 && next < q.M) fetch(next, s);
-    const W8Factors f = w8_scale<kNorm>(p, row, ss, top);
-    w8_give<kNorm, kVecs>(p, row, h, f);
+    w8_give<kNorm, kVecs>(p, row, h, w8_scale<kNorm>(p, row, ss, top, p.eps, rare), tid);
     odd ^= 1;
     if (++s == NS) s = 0, phase ^= 1;
+  }
+  if constexpr (kNorm) {
+    if (again) {
+      __syncthreads();  // `part` has been read, the marks are there
+      for (size_t row = blockIdx.x; row < q.M; row += gridDim.x)
+        if (p.scale[row] == kW8Again) w8_again<kRow, kF32>(p, row, part);
+    }
   }
 }
 

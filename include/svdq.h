@@ -471,7 +471,9 @@ svdq_status awq_quantize_weight(int N, int K, const void* W, void* qweight, void
  * front of it, in the same pass over the row:
  *   h = X + residual (float32),  residual_out = RN(h),
  *   y = h / sqrt(mean_k(h^2) + eps) * weight,  then as above on y
- * The norm reads h before its rounding to residual_out.
+ * The norm reads h before its rounding to residual_out. Any finite h is in range, also where its
+ * squares are not (such a row is scaled by a power of two first). eps = 0 and a row of zeros is
+ * 0 / 0: its scale is NaN.
  *   residual, residual_out  [M, ldr], [M, ldo] like X, both or neither (h = X);
  *                           residual_out may be residual or X itself
  *   weight                  bf16 [K], 16-byte aligned, or NULL (1)

@@ -139,6 +139,35 @@ def test_rmsnorm_rows_of_their_own(bq):
     check_norm(codes[2:3], scale[2:3], y, 40 * U)
 
 
+@TYPES
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+@pytest.mark.parametrize("M,K,weight,residual", [
+    (7, 64, False, False), (14, 3840, True, True), (9999, 64, True, True), (5001, 1040, False, False), (1501, 3840, True, True),
+    (40, 16400, True, False), (333, 16400, False, True)])
+def test_rmsnorm_rows_whose_squares_leave_float32(bq, M, K, weight, residual, eps, dtype):
+    """Rows whose squares overflow, vanish or are subnormal in float32, up to h near its largest value
+    (where h times the weight overflows too) and h subnormal, between rows of the usual size: the
+    formula's values, in both kernels, in place too. The same roundings as elsewhere: the row is
+    scaled by a power of two."""
+    sizes = torch.tensor([1.0, 1e20, 3e-25, 1.5e37, 1e-38, 2e18, 1e-12], device="cuda")[torch.arange(M) % 7]
+    x, w = draw(1, M, K).clamp_(-4, 4), (2 + draw(2, K, std=2.0)).to(BF) if weight else None
+    x = (x * sizes[:, None]).to(dtype)
+    r = (draw(3, M, K).clamp_(-4, 4) * sizes[:, None]).to(dtype) if residual else None
+    codes, scale, out = bq.w8a8_rmsnorm_quantize(x, w, r, eps=eps)
+    _, y, rel = norm_bounds(x, w, r, float(np.float32(eps)), K)
+    check_norm(codes, scale, y, rel)
+    usual = torch.arange(M, device="cuda") % 7 == 0
+    c1, s1, _ = bq.w8a8_rmsnorm_quantize(x[usual], w, None if r is None else r[usual], eps=eps)
+    if usual.sum() < 300 and M < 300:  # (the same kernel: the same order of the sums)
+        assert torch.equal(codes[usual].view(torch.uint8), c1.view(torch.uint8)) and torch.equal(scale[usual], s1)
+    if residual:
+        assert torch.equal(out, (x.float() + r.float()).to(dtype))
+        for into in (r, x):
+            rv = into.clone()
+            c2, s2, _ = bq.w8a8_rmsnorm_quantize(rv if into is x else x, w, rv if into is r else r, eps=eps, residual_out=rv)
+            assert torch.equal(rv, out) and torch.equal(c2.view(torch.uint8), codes.view(torch.uint8)) and torch.equal(s2, scale)
+
+
 # ------------------------------------------------------------------ product
 def operands(bq, M, rows, K, seed):
     x = draw(seed, M, K)
