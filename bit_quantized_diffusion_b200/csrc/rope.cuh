@@ -10,10 +10,13 @@
 // as a 64-bit binary fraction: position times that fraction modulo 2^64 is the angle's
 // fraction of a turn, the wrap of the integer product being the range reduction. The
 // fraction carries freq's 53 bits down to 2^-64 of a turn: the angle is off by 2^-52 of
-// itself and 2^-64 turns per position. Its top 32 bits are kept: the nearest quarter
-// turn, which swaps and signs, and a rest of at most an eighth either way, whose sine and
-// cosine are the first terms of their power series in float32 (x^9 and x^10; the terms
-// left out are below 2^-29).
+// itself and 2^-64 turns per position. All 64 bits go on: the nearest quarter turn, which
+// swaps and signs, and a signed rest of at most an eighth, made a float32 in two halves, so that
+// a small rest keeps its bits and a small sine, or a cosine near a quarter turn, its relative precision
+// (of the top 32 bits alone the sine of position 1 at frequency 1e-4 was off by 8e-6 of itself).
+// The rest's sine and cosine are the first terms of their power series (x^9 and x^10; what is
+// left out is below 2^-28 of the value). With U = 2^-24 the rest is off by 2.5 U of itself (conversion, 2 pi,
+// sum), the series by 2 U more, the scale by one: cosine and sine are off by less than 2^-21 of themselves.
 #pragma once
 
 #include <type_traits>
@@ -49,19 +52,23 @@ __device__ __forceinline__ uint64_t rope_fraction(double freq) {
   return __double2ull_rd(part * 18446744073709551616.0);
 }
 
-// The position's angle under a pair's fraction, in 2^-32 of a turn.
-__device__ __forceinline__ uint32_t rope_turn(long long pos, uint64_t fraction) {
-  return static_cast<uint32_t>((static_cast<uint64_t>(pos) * fraction) >> 32);
+// The position's angle under a pair's fraction, in 2^-64 of a turn.
+__device__ __forceinline__ uint64_t rope_turn(long long pos, uint64_t fraction) {
+  return static_cast<uint64_t>(pos) * fraction;
 }
 
 // Cosines and sines of two angles, each times its scale: c = (c0, c1), s = (s0, s1). Both
 // angles go through the series together, as pairs of float32.
-__device__ __forceinline__ void rope_cos_sin2(uint32_t turn0, uint32_t turn1, float2 scale, float2& c, float2& s) {
-  // an eighth on: bits 31, 30 are the nearest quarter turn, the others the rest plus an eighth
-  const uint32_t t0 = turn0 + 0x20000000u, t1 = turn1 + 0x20000000u;
-  auto rest = [](uint32_t t) { return static_cast<float>(static_cast<int>(t & 0x3FFFFFFFu) - 0x20000000); };
+__device__ __forceinline__ void rope_cos_sin2(uint64_t turn0, uint64_t turn1, float2 scale, float2& c, float2& s) {
+  // an eighth on, and half of 2^-32, which rounds the upper half: its bits 31, 30 are the nearest quarter turn,
+  // its others the rest plus an eighth; the lower half, as a signed number, is what the rest has below
+  constexpr uint64_t kOn = (1ull << 61) + (1ull << 31);
+  const uint32_t t0 = static_cast<uint32_t>((turn0 + kOn) >> 32), t1 = static_cast<uint32_t>((turn1 + kOn) >> 32);
+  auto upper = [](uint32_t t) { return static_cast<float>(static_cast<int>(t & 0x3FFFFFFFu) - 0x20000000); };
+  auto lower = [](uint64_t turn) { return static_cast<float>(static_cast<int>(static_cast<uint32_t>(turn))); };
   auto k = [](float v) { return make_float2(v, v); };
-  const float2 x = __fmul2_rn(make_float2(rest(t0), rest(t1)), k(1.4629180792671596e-9f));  // 2 pi 2^-32
+  const float2 x = __ffma2_rn(make_float2(upper(t0), upper(t1)), k(1.4629180792671596e-9f),                // 2 pi 2^-32
+                              __fmul2_rn(make_float2(lower(turn0), lower(turn1)), k(3.4061215800865545e-19f)));  // 2 pi 2^-64
   const float2 xx = __fmul2_rn(x, x);
   float2 a = __ffma2_rn(xx, k(2.7557319e-6f), k(-1.9841270e-4f));   // 1 / 9!, 1 / 7!
   a = __ffma2_rn(xx, a, k(8.3333333e-3f));                          // 1 / 5!
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) 
       RopeVec<float, V> c, s;
       if constexpr (V == 1) {
         float2 cc, ss;
-        const uint32_t turn = rope_turn(pos[0], pair[0].fraction);
+        const uint64_t turn = rope_turn(pos[0], pair[0].fraction);
         rope_cos_sin2(turn, turn, make_float2(pair[0].scale, pair[0].scale), cc, ss);
         c.e[0] = cc.x;
         s.e[0] = ss.x;

@@ -520,7 +520,8 @@ svdq_status w8a8_gated_linear(int M, int F, int K, const void* a_codes, const fl
  *            other value gives NaN in that pair), or NULL: axis 0 for all
  * scale      factor on both tables (1, or a longer context's attention factor), finite
  * The angles are formed in 64 bits, so positions may be far: an angle is off by 2^-52
- * of itself and 2^-64 turns per position before its cosine is rounded to float32.
+ * of itself and 2^-64 turns per position. Its cosine and sine are float32, each off by
+ * less than 2^-21 of itself besides, small ones too.
  *
  * svdq_rope -- turns the heads of every row:
  *   X, Y  [M, heads, head_dim] bf16 or float32, 16-byte aligned, head_dim contiguous;

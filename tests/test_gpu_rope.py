@@ -2,9 +2,9 @@
 several position axes, far and negative positions, strided and in-place heads, and the tables
 in both orders, the fused QKV projection's among them.
 
-Bounds: an angle is off by 2^-51 of itself (both sides' products) and its cosine by 2^-22
-(float32 half-turns: pi 2^-25; two steps of the function); a turned value adds three float32
-roundings and the output type's."""
+Bounds: an angle is off by 2^-51 of itself (both sides' products) and its cosine by 2^-22 + 2 U: the
+rest of a quarter turn in float32 (2.5 U of it), the power series (2 U) and the scale (U), each of a
+value below 1; a turned value adds three float32 roundings and the output type's."""
 
 import math
 
@@ -293,3 +293,30 @@ def test_heads_of_more_vectors_than_a_block(bq, dtype, D, pairs, pad, interleave
         check(y, x, pos, freq, None, 1.25, interleaved)
         assert bq.svdq_rope(x, pos, freq, scale=1.25, interleaved=interleaved, Y=x) is x
         assert torch.equal(x, y) and torch.equal(base[:, H], last)
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64], ids=["int32", "int64"])
+@pytest.mark.parametrize("M,P", [(997, 64), (997, 33), (40_000, 8)])
+@pytest.mark.parametrize("angle_major", [False, True], ids=["rows", "angle-major"])
+def test_small_angles_keep_their_precision(bq, M, P, angle_major, dtype):
+    """Cosines and sines are float32 of their own size, not of a turn: slow pairs at near positions,
+    whose sines are far below 1, and angles beside a quarter turn. The rest of a quarter turn is off
+    by 2.5 U of itself, its series by 2 U, the scale by U: below 8 U = 2^-21 of the value, and the
+    angle's own 2^-52 (and the comparison's 2^-53) and 2^-64 turns a position."""
+    freq = torch.logspace(-1, -9, P, dtype=torch.float64)
+    freq[0], freq[1] = math.pi / 2, math.pi / 2 + 1e-6
+    pos = torch.arange(-9, M - 9, dtype=dtype)
+    for scale in (1.0, 1.2079):
+        cos, sin = bq.svdq_rope_table(pos.cuda(), freq.cuda(), scale=scale, angle_major=angle_major)
+        angle = pos.double().numpy()[:, None] * freq.numpy()
+        scale = float(np.float32(scale))
+        e = scale * (np.abs(angle) * (2.0 ** -52 + 2.0 ** -53) + np.abs(pos.numpy()[:, None]) * 2.0 ** -61)
+        for got, want in ((cos, scale * np.cos(angle)), (sin, scale * np.sin(angle))):
+            got = f64(got.t() if angle_major else got)
+            assert np.all(np.abs(got - want) <= 2.0 ** -21 * np.abs(want) + e)
+    # and the rotation's: a unit vector's first coordinates
+    x = torch.zeros(M, 1, 2 * P)
+    x[..., :P] = 1.0
+    y = f64(bq.svdq_rope(x.cuda(), pos.cuda(), freq.cuda()))[:, 0]
+    e = np.abs(angle) * (2.0 ** -52 + 2.0 ** -53) + np.abs(pos.numpy()[:, None]) * 2.0 ** -61
+    assert np.all(np.abs(y[:, P:] - np.sin(angle)) <= 2.0 ** -21 * np.abs(np.sin(angle)) + e)
