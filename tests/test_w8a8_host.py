@@ -254,3 +254,15 @@ def test_rotary_layer_wants_a_position_per_axis(monkeypatch):
             rot.tables(pos)
         with pytest.raises(ValueError, match="positions"):
             rot(x, pos)
+
+
+def test_current_stream_with_and_without_torchs_short_cut(monkeypatch):
+    """The older calls' stream: the handle alone where torch gives it, else the public Stream's."""
+    from types import SimpleNamespace
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(bq, "_raw_stream", lambda device: 50 + device)
+    assert bq._stream(None) == 53
+    monkeypatch.setattr(bq, "_raw_stream", None)
+    assert bq._stream(None) == 77
+    assert bq._stream(SimpleNamespace(cuda_stream=5)) == 5 and bq._stream(9) == 9
