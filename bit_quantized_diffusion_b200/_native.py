@@ -47,8 +47,12 @@ def binding():
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(
                 f"{BINDING_PATH} is missing: build it with `python -m bit_quantized_diffusion_b200.build`")
-        import torch  # noqa: F401  (its libraries are the binding's)
-        _binding = importlib.import_module(__package__ + "._binding")
+        import torch  # its libraries are the binding's
+        try:
+            _binding = importlib.import_module(__package__ + "._binding")
+        except ImportError as e:
+            raise RuntimeError(f"{BINDING_PATH} does not load under torch {torch.__version__}: build it again with "
+                               "`python -m bit_quantized_diffusion_b200.build`") from e
     return _binding
 
 

@@ -44,6 +44,13 @@ def command(out: str = LIB, verbose_ptxas: bool = False) -> list[str]:
     return cmd
 
 
+def built_for() -> str:
+    """What a compiled binding belongs to besides its sources: this interpreter and this torch."""
+    import torch
+    return (f"{sys.implementation.cache_tag}, torch {torch.__version__}, "
+            f"C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
 def binding_command(out: str = BINDING) -> list[str]:
     import torch
     home = os.path.dirname(torch.__file__)
@@ -53,7 +60,7 @@ def binding_command(out: str = BINDING) -> list[str]:
         raise RuntimeError("no C++ compiler found")
     # libsvdq.so is found beside the binding, so both bindings share one library
     return [cxx, "-shared", "-fPIC", "-O2", "-std=c++17",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DSVDQ_BUILT_FOR="{built_for()}"',
             "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
             "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
             "-isystem", os.path.join(cuda, "include"), "-o", out, BINDING_DEPS[0],
@@ -68,12 +75,21 @@ def up_to_date(out: str = LIB, deps=DEPS) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def binding_up_to_date(out: str = BINDING, deps=BINDING_DEPS) -> bool:
+    """Newer than its sources, and built for the torch that will load it: the module holds the text of
+    built_for(). (Another torch's symbols differ, and the import would fail.)"""
+    if not up_to_date(out, deps):
+        return False
+    with open(out, "rb") as f:
+        return built_for().encode() + b"\0" in f.read()
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or not up_to_date():
         tmp = LIB + ".tmp"
         subprocess.run(command(tmp, verbose_ptxas), check=True)
         os.replace(tmp, LIB)
-    if force or not up_to_date(BINDING, BINDING_DEPS):
+    if force or not binding_up_to_date():
         tmp = BINDING + ".tmp"
         subprocess.run(binding_command(tmp), check=True)
         os.replace(tmp, BINDING)

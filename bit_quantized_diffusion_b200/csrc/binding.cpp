@@ -350,4 +350,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// the interpreter and the torch that this was compiled for (build.py looks for the text, and gives it)
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", SVDQ_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -266,3 +266,37 @@ def test_current_stream_with_and_without_torchs_short_cut(monkeypatch):
     monkeypatch.setattr(bq, "_raw_stream", None)
     assert bq._stream(None) == 77
     assert bq._stream(SimpleNamespace(cuda_stream=5)) == 5 and bq._stream(9) == 9
+
+
+def test_binding_is_rebuilt_for_another_torch(lib, tmp_path, monkeypatch):
+    """A binding newer than its sources but compiled for another torch is not up to date; this tree's is,
+    and says what it was built for."""
+    import os
+    from bit_quantized_diffusion_b200 import _native, build
+    assert build.binding_up_to_date() and _native.binding().built_for == build.built_for()
+    source, out = tmp_path / "binding.cpp", tmp_path / "_binding.so"
+    source.write_text("")
+    out.write_bytes(b"\x7fELF" + build.built_for().encode() + b"\0")
+    os.utime(source, (1, 1))
+    assert build.binding_up_to_date(str(out), [str(source)])
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")     # one text begins with the other
+    assert not build.binding_up_to_date(str(out), [str(source)])
+    monkeypatch.undo()
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    assert not build.binding_up_to_date(str(out), [str(source)])
+    monkeypatch.undo()
+    os.utime(out, (0, 0))
+    assert not build.binding_up_to_date(str(out), [str(source)])
+
+
+def test_binding_that_does_not_load_says_what_to_do(lib, monkeypatch):
+    import importlib
+    from bit_quantized_diffusion_b200 import _native
+
+    def fails(name):
+        raise ImportError("undefined symbol")
+
+    monkeypatch.setattr(_native, "_binding", None)
+    monkeypatch.setattr(importlib, "import_module", fails)
+    with pytest.raises(RuntimeError, match="build it again"):
+        _native.binding()
