@@ -7,10 +7,12 @@ rotary positions."""
 
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import prep
-from . import (awq_w4a16_linear, svdq_codes_bytes, svdq_quantize_act, svdq_quantize_act_two_level, svdq_rope,
+from . import (_stream, awq_w4a16_linear, svdq_codes_bytes, svdq_quantize_act, svdq_quantize_act_two_level, svdq_rope,
                svdq_rope_table, svdq_scales_bytes, svdq_tensor_scale, svdq_w4a4_linear, svdq_w4a4_linear_qkv_norm_rope,
                svdq_w4a4_linear_two_level, svdq_xl1_splits, w8a8_gated_linear, w8a8_linear, w8a8_quantize_act,
                w8a8_rmsnorm_quantize)
@@ -205,9 +207,29 @@ class RotaryEmbedding:
     __call__ = forward
 
 
-class W8A8Linear:
+class _Buffers:
+    """What an 8-bit layer holds between its calls, made once. It serves the thread and stream that made the
+    layer: there one forward's calls follow another's. A forward on another stream or thread, or in a
+    capture, whose replays may meet either, gets buffers of its own from its stream's (a graph's own)
+    pool, so that any number of them may run at once."""
+
+    def _own(self, device: torch.device) -> None:
+        self._home = None
+        if device.type == "cuda":
+            with torch.cuda.device(device):
+                self._home = threading.get_ident(), _stream(None)
+
+    def _at_home(self, stream) -> bool:
+        if self._home is None:
+            return True
+        thread, home = self._home
+        return (_stream(stream) == home and threading.get_ident() == thread
+                and (home == 0 or not torch.cuda.is_current_stream_capturing()))  # (the default stream cannot capture)
+
+
+class W8A8Linear(_Buffers):
     """Y = act(X W^T + bias) + residual with E4M3 rows of X and W (w8a8_quantize_act,
-    w8a8_linear)."""
+    w8a8_linear). One instance may be called on several streams and threads at once."""
 
     def __init__(self, weights: dict, bias: torch.Tensor | None, max_tokens: int, activation: str | None = None):
         self.w, self.bias, self.activation = weights, bias, activation
@@ -215,6 +237,7 @@ class W8A8Linear:
         self.max_tokens = max_tokens
         self.codes = torch.empty((max_tokens, weights["K"]), dtype=torch.float8_e4m3fn, device=dev)
         self.scale = torch.empty(max_tokens, dtype=torch.float32, device=dev)
+        self._own(dev)
 
     @classmethod
     def from_linear(cls, weight: torch.Tensor, bias: torch.Tensor | None, max_tokens: int,
@@ -227,7 +250,8 @@ class W8A8Linear:
         M = x.shape[0]
         if M > self.max_tokens:
             raise ValueError(f"{M} tokens > workspace for {self.max_tokens}")
-        codes, scale = w8a8_quantize_act(x, codes=self.codes[:M], scale=self.scale[:M], stream=stream)
+        kept = (self.codes[:M], self.scale[:M]) if self._at_home(stream) else (None, None)
+        codes, scale = w8a8_quantize_act(x, codes=kept[0], scale=kept[1], stream=stream)
         return self.forward_quantized(codes, scale, residual, y, stream)
 
     def forward_quantized(self, codes: torch.Tensor, scale: torch.Tensor, residual: torch.Tensor | None = None,
@@ -239,13 +263,14 @@ class W8A8Linear:
     __call__ = forward
 
 
-class W8A8GatedMlp:
+class W8A8GatedMlp(_Buffers):
     """A pre-norm gated feed-forward block in 8 bits, on the residual stream:
     h = x (+ residual);  out = h + down(act(gate(norm(h))) * up(norm(h))), four calls:
     norm into E4M3, the gated product, its rows into E4M3, the second projection with h added in its
     epilogue. ``up`` holds the F gate rows and then the F up rows [2F, K]; ``down`` [K, F].
     The hidden rows pass through bf16 on their way into E4M3 (their scale needs the whole
-    row, which no tile of the product holds): 2^-8 of a value beside E4M3's 2^-4."""
+    row, which no tile of the product holds): 2^-8 of a value beside E4M3's 2^-4. One instance may be
+    called on several streams and threads at once."""
 
     def __init__(self, up: dict, down: dict, norm: torch.Tensor | None, max_tokens: int, activation: str = "silu",
                  eps: float = 1e-6):
@@ -260,6 +285,7 @@ class W8A8GatedMlp:
         self.hidden = torch.empty((max_tokens, F), dtype=torch.bfloat16, device=dev)
         self.hidden_codes = torch.empty((max_tokens, F), dtype=torch.float8_e4m3fn, device=dev)
         self.scale = torch.empty((2, max_tokens), dtype=torch.float32, device=dev)
+        self._own(dev)
 
     @classmethod
     def from_linears(cls, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, norm: torch.Tensor | None,
@@ -277,14 +303,18 @@ class W8A8GatedMlp:
         M = x.shape[0]
         if M > self.max_tokens:
             raise ValueError(f"{M} tokens > workspace for {self.max_tokens}")
-        codes, scale, h = w8a8_rmsnorm_quantize(x, self.norm, residual, eps=self.eps, codes=self.codes[:M],
-                                                scale=self.scale[0, :M], residual_out=None if residual is None else y,
-                                                stream=stream)
-        hidden = w8a8_gated_linear(codes, scale, self.up["codes"], self.up["scale"], activation=self.activation,
-                                   Y=self.hidden[:M], stream=stream)
-        codes, scale = w8a8_quantize_act(hidden, codes=self.hidden_codes[:M], scale=self.scale[1, :M], stream=stream)
+        if self._at_home(stream):
+            codes, scale, hidden = self.codes[:M], self.scale[:, :M], self.hidden[:M]
+            hidden_codes = self.hidden_codes[:M]
+        else:
+            codes, scale, hidden, hidden_codes = None, (None, None), None, None
+        codes, s, h = w8a8_rmsnorm_quantize(x, self.norm, residual, eps=self.eps, codes=codes, scale=scale[0],
+                                            residual_out=None if residual is None else y, stream=stream)
+        hidden = w8a8_gated_linear(codes, s, self.up["codes"], self.up["scale"], activation=self.activation,
+                                   Y=hidden, stream=stream)
+        codes, s = w8a8_quantize_act(hidden, codes=hidden_codes, scale=scale[1], stream=stream)
         h = x if h is None else h
-        return w8a8_linear(codes, scale, self.down["codes"], self.down["scale"], residual=h,
+        return w8a8_linear(codes, s, self.down["codes"], self.down["scale"], residual=h,
                            Y=h if residual is not None else y, stream=stream)
 
     __call__ = forward

@@ -446,6 +446,66 @@ def test_chain_on_one_buffer(bq, M):
     assert torch.isfinite(want.float()).all() and bq.svdq_check_device_status() == 0
 
 
+@pytest.mark.parametrize("M", [4, 300, 1500])
+def test_one_layer_on_several_streams_at_once(bq, M):
+    """One block and one linear layer called from two threads and on two streams in turn, and captured
+    into two graphs that are replayed side by side: each call's bits are those of the call alone."""
+    import threading
+    from bit_quantized_diffusion_b200.layers import W8A8GatedMlp, W8A8Linear
+    K, F = 512, 1040
+    block = W8A8GatedMlp.from_linears(draw(1, F, K, dtype=BF, std=0.04), draw(2, F, K, dtype=BF, std=0.04),
+                                      draw(3, K, F, dtype=BF, std=0.03), None, max_tokens=M)
+    lin = W8A8Linear.from_linear(draw(4, K, K, dtype=BF, std=0.04), None, max_tokens=M)
+    x = [draw(10 + i, M, K, dtype=BF) for i in range(2)]
+    r = [draw(20 + i, M, K, dtype=BF) for i in range(2)]
+
+    def once(i, stream=None):
+        return lin(block(x[i], r[i], stream=stream), residual=r[i], stream=stream)
+
+    want = [once(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(30):
+        for i in range(2):
+            got[i].append(once(i, streams[i]))
+        got[0].append(once(0))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(t, want[i]) for t in got[i])
+    out, errors = [None, None], []
+
+    def run(i):
+        try:
+            for _ in range(30):  # both threads on the default stream
+                out[i] = once(i)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not errors and all(torch.equal(out[i], want[i]) for i in range(2))
+    graphs, out = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out.append(once(i))
+        graphs.append(graph)
+    for t in out:
+        t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        once(0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[i], want[i]) for i in range(2))
+    assert bq.svdq_check_device_status() == 0
+
+
 def test_offsets_beyond_32_bits(bq):
     """Rows, outputs and residuals whose elements number over 2^32: the last rows and one in the
     middle agree with calls on those rows alone."""

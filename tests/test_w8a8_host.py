@@ -300,3 +300,61 @@ def test_binding_that_does_not_load_says_what_to_do(lib, monkeypatch):
     monkeypatch.setattr(importlib, "import_module", fails)
     with pytest.raises(RuntimeError, match="build it again"):
         _native.binding()
+
+
+def test_layers_share_no_buffers_across_streams_threads_and_captures(monkeypatch):
+    """A layer's buffers serve the thread and stream that made it; a call on another stream, from another
+    thread or in a capture takes none of them."""
+    import threading
+    given, state = [], {"current": 5, "capturing": False}
+
+    def fresh(*shape, dtype=E4):
+        return torch.zeros(shape, dtype=dtype)
+
+    def quant(x, codes=None, scale=None, stream=None):
+        given.extend((codes, scale))
+        return (fresh(*x.shape) if codes is None else codes), (fresh(x.shape[0], dtype=F32) if scale is None else scale)
+
+    def norm(x, weight=None, residual=None, eps=1e-6, codes=None, scale=None, residual_out=None, stream=None):
+        return (*quant(x, codes, scale), residual_out)
+
+    def gated(c, s, w, ws, bias=None, activation="silu", out_dtype=BF, Y=None, stream=None):
+        given.append(Y)
+        return fresh(c.shape[0], w.shape[0] // 2, dtype=BF) if Y is None else Y
+
+    def linear(c, s, w, ws, bias=None, residual=None, activation=None, out_dtype=BF, Y=None, stream=None):
+        return fresh(c.shape[0], w.shape[0], dtype=BF) if Y is None else Y
+
+    for name, fn in (("w8a8_rmsnorm_quantize", norm), ("w8a8_quantize_act", quant), ("w8a8_gated_linear", gated),
+                     ("w8a8_linear", linear)):
+        monkeypatch.setattr(L, name, fn)
+    monkeypatch.setattr(L, "_stream", lambda s: state["current"] if s is None else s, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    K, F = 32, 64
+    w = {"codes": torch.zeros(2 * F, K).to(E4), "scale": torch.ones(2 * F), "N": 2 * F, "K": K}
+    down = {"codes": torch.zeros(K, F).to(E4), "scale": torch.ones(K), "N": K, "K": F}
+    for layer, count in ((L.W8A8Linear(w, None, max_tokens=8), 2), (L.W8A8GatedMlp(w, down, None, max_tokens=8), 5)):
+        layer._home = threading.get_ident(), 5
+        own = {t.untyped_storage().data_ptr() for t in vars(layer).values() if isinstance(t, torch.Tensor)}
+
+        def shared(run):
+            given.clear()
+            run()
+            assert len(given) == count
+            return [t is not None and t.untyped_storage().data_ptr() in own for t in given]
+
+        x = torch.zeros(5, K, dtype=BF)
+        assert all(shared(lambda: layer(x))) and all(shared(lambda: layer(x, stream=5)))
+        assert not any(shared(lambda: layer(x, stream=6)))
+
+        def elsewhere():
+            t = threading.Thread(target=layer, args=(x,))
+            t.start()
+            t.join()
+
+        assert not any(shared(elsewhere))
+        for key, value in (("current", 6), ("capturing", True)):
+            before = state[key]
+            state[key] = value
+            assert not any(shared(lambda: layer(x)))
+            state[key] = before
