@@ -229,10 +229,12 @@ class _Buffers:
 
 class W8A8Linear(_Buffers):
     """Y = act(X W^T + bias) + residual with E4M3 rows of X and W (w8a8_quantize_act,
-    w8a8_linear). One instance may be called on several streams and threads at once."""
+    w8a8_linear). Y, and so the residual, is bf16 or float32 (out_dtype). One instance may be called on
+    several streams and threads at once."""
 
-    def __init__(self, weights: dict, bias: torch.Tensor | None, max_tokens: int, activation: str | None = None):
-        self.w, self.bias, self.activation = weights, bias, activation
+    def __init__(self, weights: dict, bias: torch.Tensor | None, max_tokens: int, activation: str | None = None,
+                 out_dtype: torch.dtype = torch.bfloat16):
+        self.w, self.bias, self.activation, self.out_dtype = weights, bias, activation, out_dtype
         dev = weights["codes"].device
         self.max_tokens = max_tokens
         self.codes = torch.empty((max_tokens, weights["K"]), dtype=torch.float8_e4m3fn, device=dev)
@@ -241,9 +243,9 @@ class W8A8Linear(_Buffers):
 
     @classmethod
     def from_linear(cls, weight: torch.Tensor, bias: torch.Tensor | None, max_tokens: int,
-                    activation: str | None = None):
+                    activation: str | None = None, out_dtype: torch.dtype = torch.bfloat16):
         """From an nn.Linear's weight [N, K] bf16 and bias [N] bf16 or None."""
-        return cls(prep.prepare_w8a8_weights(weight), bias, max_tokens, activation)
+        return cls(prep.prepare_w8a8_weights(weight), bias, max_tokens, activation, out_dtype)
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
@@ -258,7 +260,7 @@ class W8A8Linear(_Buffers):
                           y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The product alone, on rows quantized already (by a norm that feeds several layers, say)."""
         return w8a8_linear(codes, scale, self.w["codes"], self.w["scale"], self.bias, residual=residual,
-                           activation=self.activation, Y=y, stream=stream)
+                           activation=self.activation, out_dtype=self.out_dtype, Y=y, stream=stream)
 
     __call__ = forward
 

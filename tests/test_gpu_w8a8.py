@@ -446,6 +446,21 @@ def test_chain_on_one_buffer(bq, M):
     assert torch.isfinite(want.float()).all() and bq.svdq_check_device_status() == 0
 
 
+@TYPES
+@pytest.mark.parametrize("M", [1, 60, 300])
+def test_linear_layer_on_a_stream_of_either_type(bq, M, dtype):
+    """W8A8Linear onto a residual stream of its output's type, new and in place: the calls under it, bit for bit."""
+    from bit_quantized_diffusion_b200.layers import W8A8Linear
+    K, N = 272, 528
+    w, b = draw(1, N, K, dtype=BF, std=0.04), draw(2, N, dtype=BF, std=0.1)
+    x, r = draw(3, M, K, dtype=dtype), draw(4, M, N, dtype=dtype)
+    lin = W8A8Linear.from_linear(w, b, max_tokens=M, out_dtype=dtype)
+    y = lin(x, residual=r)
+    assert y.dtype == dtype
+    assert torch.equal(y, bq.w8a8_linear(*bq.w8a8_quantize_act(x), *bq.w8a8_quantize_act(w), b, residual=r, out_dtype=dtype))
+    assert lin(x, residual=r, y=r) is r and torch.equal(r, y)
+
+
 @pytest.mark.parametrize("M", [4, 300, 1500])
 def test_one_layer_on_several_streams_at_once(bq, M):
     """One block and one linear layer called from two threads and on two streams in turn, and captured
