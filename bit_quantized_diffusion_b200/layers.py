@@ -271,14 +271,16 @@ class W8A8GatedMlp(_Buffers):
     norm into E4M3, the gated product, its rows into E4M3, the second projection with h added in its
     epilogue. ``up`` holds the F gate rows and then the F up rows [2F, K]; ``down`` [K, F].
     The hidden rows pass through bf16 on their way into E4M3 (their scale needs the whole
-    row, which no tile of the product holds): 2^-8 of a value beside E4M3's 2^-4. One instance may be
-    called on several streams and threads at once."""
+    row, which no tile of the product holds): 2^-8 of a value beside E4M3's 2^-4. ``up_bias`` [2F] and
+    ``down_bias`` [K] are bf16 or None. The stream is bf16 or float32, out of its type. One instance may
+    be called on several streams and threads at once."""
 
     def __init__(self, up: dict, down: dict, norm: torch.Tensor | None, max_tokens: int, activation: str = "silu",
-                 eps: float = 1e-6):
+                 eps: float = 1e-6, up_bias: torch.Tensor | None = None, down_bias: torch.Tensor | None = None):
         if up["N"] != 2 * down["K"] or up["K"] != down["N"]:
             raise ValueError("up must be [2F, K] and down [K, F]")
         self.up, self.down, self.norm = up, down, norm
+        self.up_bias, self.down_bias = up_bias, down_bias
         self.activation, self.eps = activation, float(eps)
         dev = up["codes"].device
         K, F = up["K"], down["K"]
@@ -291,16 +293,21 @@ class W8A8GatedMlp(_Buffers):
 
     @classmethod
     def from_linears(cls, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, norm: torch.Tensor | None,
-                     max_tokens: int, activation: str = "silu", eps: float = 1e-6):
-        """From the gate, up [F, K] and down [K, F] weights, bf16; norm [K] bf16 or None."""
+                     max_tokens: int, activation: str = "silu", eps: float = 1e-6,
+                     gate_bias: torch.Tensor | None = None, up_bias: torch.Tensor | None = None,
+                     down_bias: torch.Tensor | None = None):
+        """From the gate, up [F, K] and down [K, F] weights, bf16; norm [K] bf16 or None; biases bf16 or
+        None, of gate and up both or neither."""
         if gate.shape != up.shape:
             raise ValueError("gate and up must be equal [F, K] weights")
+        if (gate_bias is None) != (up_bias is None):
+            raise ValueError("gate and up have a bias both or neither")
         return cls(prep.prepare_w8a8_weights(torch.cat([gate, up])), prep.prepare_w8a8_weights(down), norm,
-                   max_tokens, activation, eps)
+                   max_tokens, activation, eps, None if gate_bias is None else torch.cat([gate_bias, up_bias]), down_bias)
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
-        """x (and residual) [M, K] bf16 -> [M, K] bf16; with a residual, y (or a new tensor)
+        """x (and residual) [M, K] bf16 or float32 -> [M, K] of its type; with a residual, y (or a new tensor)
         also holds h between the calls. y may be x or residual."""
         M = x.shape[0]
         if M > self.max_tokens:
@@ -312,11 +319,11 @@ class W8A8GatedMlp(_Buffers):
             codes, scale, hidden, hidden_codes = None, (None, None), None, None
         codes, s, h = w8a8_rmsnorm_quantize(x, self.norm, residual, eps=self.eps, codes=codes, scale=scale[0],
                                             residual_out=None if residual is None else y, stream=stream)
-        hidden = w8a8_gated_linear(codes, s, self.up["codes"], self.up["scale"], activation=self.activation,
-                                   Y=hidden, stream=stream)
+        hidden = w8a8_gated_linear(codes, s, self.up["codes"], self.up["scale"], self.up_bias,
+                                   activation=self.activation, Y=hidden, stream=stream)
         codes, s = w8a8_quantize_act(hidden, codes=hidden_codes, scale=scale[1], stream=stream)
         h = x if h is None else h
-        return w8a8_linear(codes, s, self.down["codes"], self.down["scale"], residual=h,
-                           Y=h if residual is not None else y, stream=stream)
+        return w8a8_linear(codes, s, self.down["codes"], self.down["scale"], self.down_bias, residual=h,
+                           out_dtype=x.dtype, Y=h if residual is not None else y, stream=stream)
 
     __call__ = forward

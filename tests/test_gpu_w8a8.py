@@ -448,6 +448,35 @@ def test_chain_on_one_buffer(bq, M):
 
 @TYPES
 @pytest.mark.parametrize("M", [1, 60, 300])
+def test_gated_block_with_biases(bq, M, dtype):
+    """Gate, up and down with a bias each, on a stream of either type: the block against its parts in
+    float64 through the kernels' own codes, and in place."""
+    from bit_quantized_diffusion_b200.layers import W8A8GatedMlp
+    K, F = 272, 656
+    gate, up, down = (draw(i, *s, dtype=BF, std=0.04) for i, s in ((1, (F, K)), (2, (F, K)), (3, (K, F))))
+    bg, bu, bd = (draw(i, n, dtype=BF, std=0.5) for i, n in ((4, F), (5, F), (6, K)))
+    x, r = draw(7, M, K, dtype=dtype), draw(8, M, K, dtype=dtype, std=2.0)
+    block = W8A8GatedMlp.from_linears(gate, up, down, None, M, "gelu", gate_bias=bg, up_bias=bu, down_bias=bd)
+    y = block(x, r)
+    assert y.dtype == dtype
+    h, n, rel = norm_bounds(x, None, r, 1e-6, K)
+    check_norm(block.codes, block.scale[0], n, rel)
+    z, ez = product_bound(block.codes, block.scale[0], block.up["codes"], block.up["scale"], torch.cat([bg, bu]), K)
+    g, eg = act_bound(z[:, :F], ez[:, :F], "gelu")
+    hidden, e = g * z[:, F:], np.abs(g) * ez[:, F:] + np.abs(z[:, F:]) * eg + eg * ez[:, F:]
+    assert np.all(np.abs(f64(block.hidden) - hidden) <= 1.01 * e + (2.0 ** -8 + 2 * U) * (np.abs(hidden) + e))
+    z, ez = product_bound(block.hidden_codes, block.scale[1], block.down["codes"], block.down["scale"], bd, F)
+    # h goes through the stream's type on its way to the second projection
+    want, e = z + h, ez + (half_step(dtype) + 2 * U) * np.abs(h)
+    assert np.all(np.abs(f64(y) - want) <= 1.01 * e + (half_step(dtype) + 2 * U) * (np.abs(want) + e))
+    alone = block(x)
+    assert alone.dtype == dtype and block(x, y=x) is x and torch.equal(x, alone)
+    with pytest.raises(ValueError, match="both or neither"):
+        W8A8GatedMlp.from_linears(gate, up, down, None, M, gate_bias=bg)
+
+
+@TYPES
+@pytest.mark.parametrize("M", [1, 60, 300])
 def test_linear_layer_on_a_stream_of_either_type(bq, M, dtype):
     """W8A8Linear onto a residual stream of its output's type, new and in place: the calls under it, bit for bit."""
     from bit_quantized_diffusion_b200.layers import W8A8Linear
