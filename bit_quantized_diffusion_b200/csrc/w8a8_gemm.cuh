@@ -823,9 +823,11 @@ __global__ void __launch_bounds__(kWsThreads, 2)
 constexpr int kWvMaxM = 16;
 constexpr int kWvUnroll = 4;  // 64-byte steps whose loads are on their way together
 
+// (Not the read-only path, here and for the tokens: the grid before, which may have made either operand, can
+// still be writing when this one starts.)
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* at) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(at));
   return v;
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(512) w8a8_gemv_kernel(const WvParams p) {
 #pragma unroll
       for (int j = 0; j < kTokens8; ++j)
         b[u][j] = in && 8 * j + g < p.M
-                      ? __ldg(reinterpret_cast<const uint4*>(p.a + (8 * j + g) * K + k + 16 * t))
+                      ? *reinterpret_cast<const uint4*>(p.a + (8 * j + g) * K + k + 16 * t)
                       : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll

@@ -550,6 +550,24 @@ def test_one_layer_on_several_streams_at_once(bq, M):
     assert bq.svdq_check_device_status() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1040, 2064), (16, 272, 1040), (40, 528, 1040), (300, 528, 656)])
+def test_both_operands_made_just_before(bq, M, N, K):
+    """Weight and tokens quantized into the same buffers again and again, each product right behind: the
+    bits of operands that nothing writes to."""
+    ws, xs = [draw(i, N, K, dtype=BF, std=0.04) for i in range(5)], [draw(9 + i, M, K, dtype=BF) for i in range(5)]
+    want = [bq.w8a8_linear(*bq.w8a8_quantize_act(x), *bq.w8a8_quantize_act(w)) for x, w in zip(xs, ws)]
+    codes, scale = bq.w8a8_quantize_act(xs[0])
+    w_codes, w_scale = bq.w8a8_quantize_act(ws[0])
+    torch.cuda.synchronize()
+    got = []
+    for step in range(100):
+        bq.w8a8_quantize_act(xs[step % 5], codes=codes, scale=scale)
+        bq.w8a8_quantize_act(ws[step % 5], codes=w_codes, scale=w_scale)
+        got.append(bq.w8a8_linear(codes, scale, w_codes, w_scale))
+    for step, y in enumerate(got):
+        assert torch.equal(y, want[step % 5]), step
+
+
 def test_offsets_beyond_32_bits(bq):
     """Rows, outputs and residuals whose elements number over 2^32: the last rows and one in the
     middle agree with calls on those rows alone."""
