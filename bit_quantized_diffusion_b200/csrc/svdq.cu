@@ -1175,7 +1175,8 @@ bool stream_shares(const DeviceInfo* d, const StreamPlan& s, int splits) {
 // saves, both growing with T; a stage's way in, longer in wider clusters, or all SMs' share of
 // the memory; CTAs that share an SM end one after the other. Fitted to 222 shapes (up to 104 row
 // tiles, K 512 to 15360, 4 to 128 tokens) timed with every count: the choice is 0.3 % slower than the
-// fastest on average, 9 % at worst. 64 tokens, (K, N): (1024, 5760) takes 5.0, 5.8, 6.5 us with
+// fastest on average, 9 % at worst; on 61 shapes outside them (106 to 148 row tiles, K 4096 to 15360) that it
+// splits, 1.7 % slower than the faster of split and whole on average, 7 % at worst. 64 tokens, (K, N): (1024, 5760) takes 5.0, 5.8, 6.5 us with
 // 1, 2, 4; (3840, 3840) 10.3, 9.3, 8.4, 9.5 with 1, 2, 4, 8; (12288, 1024) 28.4, 18.1, 11.4, 8.9.
 long long stream_cost(const DeviceInfo* d, const StreamPlan& s, int splits) {
   long long stage = 280;
@@ -1288,12 +1289,12 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   if (M <= kWvMaxM && K <= (M <= 8 ? 4096 : 2048) && N / (gated ? 8 : 16) <= 2 * d->num_sms)
     return launch_w8a8_gemv(d, gated, p, a_codes, w_codes, Y, ldy, stream);
   // Few tokens stream the weight (64 tokens, streamed / in CTA pairs: K = N = 1024 4.8 / 4.7 us,
-  // K = 1024, N = 15360 7.4 / 10.4). Above 64 only where the row tiles reach three in five SMs, or K
-  // is long: the epilogue of a tile grows with the tokens (128 tokens: K = N = 1024 6.1 / 4.6, K = 2048,
-  // N = 3840 8.0 / 7.3, K = 1024, N = 15360 10.2 / 11.1, K = 3840,
-  // N = 2560 9.0 / 9.1, N = 15360 17.1 / 20.9).
+  // K = 1024, N = 15360 7.4 / 10.4). Above 64 only where the row tiles reach three in five SMs: the
+  // epilogue of a tile grows with the tokens (128 tokens: K = N = 1024 6.1 / 4.6, K = 3840, N = 3840 9.7 / 9.0,
+  // N = 10240 14.0 / 12.4, N = 12800 14.0 / 13.9, N = 15360 14.0 / 15.8; K = 1040, N = 15360 9.9 / 11.2), or
+  // by what the split of a long K saves (below).
   const StreamPlan plan = stream_plan(d, gated, M, N, K);
-  if (M <= 64 || (M <= kWsMaxT && (5 * plan.tiles >= 3ll * d->num_sms || K >= 3500)))
+  if (M <= 64 || (M <= kWsMaxT && 5 * plan.tiles >= 3ll * d->num_sms))
     return launch_w8a8_stream(d, gated, p, plan, a_codes, w_codes, Y, ldy, stream);
   // The tile's width: the one whose waves of tiles over the CTA pairs take least, a stage
   // of K costing its operands' way in, 256 + bn rows per pair (at 256 columns that equals its
@@ -1315,11 +1316,12 @@ svdq_status w8a8_linear_impl(bool gated, int M, int N, int K, const void* a_code
   if (best < 0) return SVDQ_ERR_UNSUPPORTED;
   // A long K over few tiles leaves most pairs idle, while clusters that split K reach every SM. Both
   // sides in clocks: the operands' way in, and, for the clusters, the sum over them and, past eight
-  // of the widest, their waiting for whole groups of SMs (M, K, N = 340, 12512, 64: 9.1 us against
-  // 18.9 in pairs; 512, 15360, 256: 12.3 and 21.6; 256, 15360, 3840: 29.1 and 27.2; 200, 4096, 1024: 9.7
-  // and 8.5).
+  // of the widest, their waiting for whole groups of SMs. Set on 399 shapes timed both ways (65 to 1024
+  // tokens, K 2048 to 15360, N 64 to 10240): 0.4 % slower than the faster one on average, 18 % at worst (72,
+  // 2048, 272). (M, K, N), streamed / in pairs: (128, 5120, 3840) 10.2 / 10.6 and (128, 5120, 5120) 13.7 /
+  // 11.7; (340, 4096, 512) 8.1 / 8.8, 1024 12.6 / 9.0; (768, 4096, 1024) 12.6 / 9.4; (768, 12512, 144) 11.1 / 19.5.
   const long long clusters = plan.tiles * plan.token_tiles;
-  const long long split_cost = (plan.ktiles + plan.splits - 1) / plan.splits * (128ll + plan.T) * 3 + 3000 +
+  const long long split_cost = (plan.ktiles + plan.splits - 1) / plan.splits * (128ll + plan.T) * 3 + 4500 +
                                (plan.splits == 8 && clusters > 8 ? 5000 : 0);
   if (plan.splits > 1 && split_cost < best * plan.ktiles)
     return launch_w8a8_stream(d, gated, p, plan, a_codes, w_codes, Y, ldy, stream);
