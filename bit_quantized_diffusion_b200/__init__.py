@@ -444,7 +444,8 @@ def svdq_rope(X: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, axis
     positions[m, axis[i]] * freq[i]. positions int32 or int64 [M] or [M, axes]; freq float64
     [pairs] (prep.rope_frequencies), 2 pairs <= D, the other columns copied; axis int32 [pairs]
     or None (0). Pairs are columns (2i, 2i + 1) if interleaved, else (i, i + pairs). ``scale``
-    multiplies cosine and sine. Y may be X (in place)."""
+    multiplies cosine and sine. X and Y start on 16-byte boundaries, their row and head strides are
+    even. Y may be X (in place)."""
     return N.binding().svdq_rope(X, positions, freq, axis, scale, interleaved, Y, stream)
 
 

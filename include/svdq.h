@@ -481,7 +481,9 @@ svdq_status awq_quantize_weight(int N, int K, const void* W, void* qweight, void
  *
  * w8a8_linear -- the product with its epilogue:
  *   Y[m,n] = act((sum_k a[m,k] w[n,k]) a_scale[m] w_scale[n] + bias[n]) + residual[m,n]
- * float32 sums, one rounding to Y's type at the end.
+ * float32 sums, one rounding to Y's type at the end. The activations go through a fast exponential
+ * of e = -z (SiLU) or -1.6 (z + 0.0447 z^3) (GELU): off by (2.4 |e| + 10) 2^-24 of SiLU(z) and
+ * (7.4 |e| + 10) 2^-24 of GELU(z), and 0 where they are below 1e-35.
  *   a_codes [M, K], a_scale [M], w_codes [N, K], w_scale [N]
  *   bias      bf16 [N] or NULL
  *   residual  [M, ldr] of Y's type or NULL; may be Y itself (with ldr == ldy)

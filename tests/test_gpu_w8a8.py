@@ -306,6 +306,24 @@ def test_activations_far_out(bq):
             assert np.all(np.isfinite(y)) and np.all(np.abs(y - want) <= 64 * U * np.abs(want) + 1e-30 * scale)
 
 
+@pytest.mark.parametrize("M", [1, 20, 130])
+def test_activations_to_their_last_bits(bq, M):
+    """float32 outputs of z that is exact (one product of ones, times its column's scale), in every kernel.
+    exp(e) in 2 + 1.17 |e| units of its last place, 2 U each at most, the sum and the quotient in 6 U:
+    (2.4 |e| + 10) U of SiLU, where e is exact; GELU's e has five roundings of its own, 5 |e| U more.
+    A quotient by more than 2^126 may be 0."""
+    N = 1040
+    z = torch.cat([torch.linspace(-30, 12, N - 32), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-3, -1e-3, 80.0, -80.0]).repeat(4)]).cuda()
+    a, w = torch.zeros(M, 16, device="cuda"), torch.zeros(N, 16, device="cuda")
+    a[:, 0] = w[:, 0] = 1.0
+    x = f64(z)
+    for act, e, own in (("silu", np.abs(x), 2.4), ("gelu", np.abs(1.5957691216057308 * (x + 0.044715 * x ** 3)), 7.4)):
+        y = bq.w8a8_linear(a.to(E4), torch.ones(M, device="cuda"), w.to(E4), z, activation=act, out_dtype=F32)
+        # (in the form of the exponential: 1 + tanh cancels far out)
+        want = x / (1.0 + np.exp(np.minimum(e, 700.0) * -np.sign(x)))
+        assert np.all(np.abs(f64(y) - want) <= (own * e + 10) * U * np.abs(want) + 1e-35)
+
+
 # ------------------------------------------------------------------ use
 @pytest.mark.parametrize("M", [1, 24, 200])
 def test_graphs_streams_and_repeats(bq, M):
