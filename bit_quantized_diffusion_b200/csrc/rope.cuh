@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
 // cos, sin as [M, P]: a thread keeps V adjacent pairs, their fractions in registers, and
 // walks down the rows, four at a time. Its pairs' positions: one per row where there is one
 // axis, two where its pairs lie on two (so that no lane of a warp takes another way), else one
-// per pair. 131072 rows of 64 pairs, 67.6 MB: 14.8 us, 4.6 TB/s, the stores sharing the time
-// with 25 instructions an angle (40.4 us with sincospi of a float64 angle's fraction).
+// per pair. 131072 rows of 64 pairs, 67.6 MB: 15.4 us, 4.4 TB/s (a plain fill: 3.7), issue
+// slots 60 % busy, from int64 positions the same within 1 % (40.4 us with sincospif of a float32 half-turn).
 template <int V, typename Pos>
 __global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) {
   const int nq = p.P / V, per_row = min(nq, 256), rows = 256 / per_row;
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(256, 4) rope_table_kernel(const RopeParams p) 
 }
 
 // cos, sin as [P, M]: neighbouring threads take neighbouring rows, a block kRopeTablePairs
-// pairs, whose fractions are made once, in shared memory (100000 rows of 64 pairs, 51.6 MB: 14.3 us).
+// pairs, whose fractions are made once, in shared memory (100000 rows of 64 pairs, 51.6 MB: 14.0 us).
 constexpr int kRopeTablePairs = 8;
 __global__ void __launch_bounds__(256) rope_table_angle_major_kernel(const RopeParams p) {
   __shared__ RopePair pairs[kRopeTablePairs];

@@ -1175,9 +1175,10 @@ bool stream_shares(const DeviceInfo* d, const StreamPlan& s, int splits) {
 // saves, both growing with T; a stage's way in, longer in wider clusters, or all SMs' share of
 // the memory; CTAs that share an SM end one after the other. Fitted to 222 shapes (up to 104 row
 // tiles, K 512 to 15360, 4 to 128 tokens) timed with every count: the choice is 0.3 % slower than the
-// fastest on average, 9 % at worst; on 61 shapes outside them (106 to 148 row tiles, K 4096 to 15360) that it
-// splits, 1.7 % slower than the faster of split and whole on average, 7 % at worst. 64 tokens, (K, N): (1024, 5760) takes 5.0, 5.8, 6.5 us with
-// 1, 2, 4; (3840, 3840) 10.3, 9.3, 8.4, 9.5 with 1, 2, 4, 8; (12288, 1024) 28.4, 18.1, 11.4, 8.9.
+// fastest on average, 9 % at worst; on 61 shapes beyond them (106 to 148 row tiles, K 4096 to
+// 15360) that it splits, 1.7 % slower than the faster of split and whole on average, 7 % at worst. 64
+// tokens, (K, N): (1024, 5760) takes 5.0, 5.8, 6.5 us with 1, 2, 4; (3840, 3840) 10.3, 9.3, 8.4, 9.5 with
+// 1, 2, 4, 8; (12288, 1024) 28.4, 18.1, 11.4, 8.9.
 long long stream_cost(const DeviceInfo* d, const StreamPlan& s, int splits) {
   long long stage = 280;
   for (int i = splits; i > 1; i /= 2) stage += 40;
@@ -1388,7 +1389,8 @@ svdq_status w8a8_quantize_impl(bool norm, int M, int K, const void* X, int ldx, 
   // The ring, where every SM gets rows enough: as many blocks as keep two rows and the weight
   // in shared memory, up to 1024 threads an SM. 4608 rows of 3840: bf16 with residual 22.4 us
   // against 22.7 without the ring, float32 38.1 against 44.0; 4096 of 15360, codes alone, 30.3
-  // against 35.0 (with more rows ahead 32.2).
+  // against 35.0 (with more rows ahead 32.2). 9999 rows of 64 in place 6.4 against 11.2; but 20000 of 2048 in
+  // place, bf16, 53.0 against 45.9.
   const size_t weight_bytes = weight ? static_cast<size_t>(K) * 4 : 0;
   const size_t row_bytes = static_cast<size_t>(K) * (f32 ? 4 : 2) * (residual ? 2 : 1);
   size_t blocks = kW8RingBytes / (kW8RingStages * row_bytes + weight_bytes + kW8RingOwn);

@@ -24,8 +24,10 @@
 //              memory -> scales, bias, activation, residual -> memory
 // Bound by the tensor cores and, over many launches, by the power cap: gated, 4608 x 3840 x
 // 10240, 725 GFLOP, takes 229 us alone (3.17 PFLOP/s at 1.9 GHz) and 277-286 us in a row
-// (1.15-1.25 GHz at 990 W); 4096 x 15360 x 3840 168 us alone (2.87 PFLOP/s), 207-215 in a row.
-// Few columns or a short K: by the epilogue and by what a tile costs to start.
+// (1.15-1.25 GHz at 990 W); 4096 x 15360 x 3840 168 us alone (2.87 PFLOP/s), 207-220 in a row.
+// Few columns or a short K: by the epilogue and by what a tile costs to start. Up to some 1000 rows: by
+// the way of the operands through L2, since narrow tiles, or few, read A again for each (256 x 3840 x 3840
+// 9.1 us, 256 x 15360 x 3840 23.1, gated 256 x 3840 x 10240 27; the memory's time is 3.0, 10.2, 12.9).
 // Tensor memory holds two accumulators of up to 256 columns, so a tile's epilogue runs under
 // the next tile's MMAs.
 #pragma once
@@ -822,7 +824,8 @@ __global__ void __launch_bounds__(kWsThreads, 2)
 // order, so a lane's 16 bytes of a row are the fragments of two MMAs as they lie there, and
 // its 16 bytes of a token match them: neither operand passes through shared memory. Warps
 // take every other 64 bytes of K; their partial sums meet in shared memory in a fixed order.
-// One token, K = N = 3840, 14.8 MB: 5.9 us, of which an empty launch is 2.2.
+// One token, K = N = 3840, 14.8 MB: 5.7 us, of which an empty launch is 2.2; 240 blocks leave some SMs
+// two of them and others one.
 constexpr int kWvMaxM = 16;
 constexpr int kWvUnroll = 4;  // 64-byte steps whose loads are on their way together
 

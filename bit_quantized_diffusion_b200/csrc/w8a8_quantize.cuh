@@ -8,9 +8,10 @@
 // The norm's factor is one number per row, so max |y| = rsqrt(...) max |h weight|:
 // both reductions (the sum of squares, the maximum) run over the same registers and
 // meet in one block-wide exchange; the row is read once and kept in registers. Bound by
-// HBM: 4608 rows of 3840 with residual and norm, bf16, 123.9 MB: 22.5 us, 5.5 TB/s; 4096 rows of
-// 15360, codes alone, 188.8 MB: 30.4 us, 6.2 TB/s. Rows that only pass the norm come closer to the
-// instructions (4608 of 3840, 53 MB: 13.9 us). The
+// HBM: 4608 rows of 3840 with residual and norm, bf16, 123.9 MB: 22.6 us, 5.5 TB/s; 4096 rows of
+// 15360, codes alone, 188.8 MB: 30.3 us, 6.2 TB/s. Rows that only pass the norm (4608 of 3840, 53 MB: 13.9
+// us, 3.8 TB/s, issue slots 55 % busy) are held by what every thread repeats for its 30 values: the
+// wait, the exchange and its barrier, a square root and a division. The
 // floor 2^-100 keeps 448 / t finite, so an all-zero row has scale 2^-100 / 448 and
 // codes 0 and no case of its own. The maximum is taken on the bits of |y|, where NaN
 // is above infinity is above every number: a row that holds NaN has scale NaN. Rows whose squares leave

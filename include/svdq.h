@@ -475,7 +475,7 @@ svdq_status awq_quantize_weight(int N, int K, const void* W, void* qweight, void
  * squares are not (such a row is scaled by a power of two first). eps = 0 and a row of zeros is
  * 0 / 0: its scale is NaN.
  *   residual, residual_out  [M, ldr], [M, ldo] like X, both or neither (h = X);
- *                           residual_out may be residual or X itself
+ *                           residual_out may be residual or X itself (with its stride)
  *   weight                  bf16 [K], 16-byte aligned, or NULL (1)
  *   eps                     finite, >= 0
  *
