@@ -1,9 +1,9 @@
 """User-facing layers over the C ABI: the SVDQ W4A4 linear and the AWQ W4A16
 linear (the ``SVDQW4A4Linear`` / ``AWQW4A16Linear`` runtime layers of the
 Diffusers blog, "quantization_config"), with preallocated workspaces so a
-forward call is two (or one) library calls and no allocation; the 8-bit linear
-and gated feed-forward block for layers that lose too much in four bits; and
-rotary positions."""
+forward call is two (or one) library calls and no allocation (one forward of an
+instance at a time); the 8-bit linear and gated feed-forward block for layers
+that lose too much in four bits; and rotary positions."""
 
 from __future__ import annotations
 

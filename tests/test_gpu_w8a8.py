@@ -139,6 +139,18 @@ def test_rmsnorm_rows_of_their_own(bq):
     check_norm(codes[2:3], scale[2:3], y, 40 * U)
 
 
+@pytest.mark.parametrize("M", [4, 9999])
+def test_rmsnorm_of_zeros_without_eps(bq, M):
+    """0 / 0: NaN in the rows of zeros alone, in both kernels."""
+    x = draw(1, M, 64, dtype=BF)
+    clean = bq.w8a8_rmsnorm_quantize(x, eps=0.0)
+    x[2::3] = 0.0
+    codes, scale, _ = bq.w8a8_rmsnorm_quantize(x, eps=0.0)
+    zero = torch.arange(M, device="cuda") % 3 == 2
+    assert scale[zero].isnan().all() and torch.equal(scale[~zero], clean[1][~zero])
+    assert torch.equal(codes[~zero].view(torch.uint8), clean[0][~zero].view(torch.uint8))
+
+
 @TYPES
 @pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
 @pytest.mark.parametrize("M,K,weight,residual", [
